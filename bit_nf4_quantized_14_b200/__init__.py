@@ -9,6 +9,9 @@ include/qlora_nf4.h:
     linear_fwd(X, q, A, B, alpha)    -> (Y, U)        (qlora_linear_fwd)
     linear_bwd(dY, X, q, A, B, alpha, U) -> (dX, dA, dB)   (qlora_linear_bwd)
     codebook_quantize / codebook_dequantize / codebook_stats   (qlora_codebook_*)
+    codebook_linear(X, codes, absmax, N, levels), linear_single(X, q) -> Y   (qlora_codebook_linear)
+    rotary(q, k, RotaryConfig(...), positions)  -> (q', k')   (qlora_rope; autograd.rotary)
+    vocab_loss(X, W, targets, ...)   -> (loss, dX)    (qlora_vocab_loss; autograd.vocab_loss)
     adamw_step, paged_empty, paged_prefetch   (qlora_adamw_step, qlora_paged_*; optim.PagedAdamW)
 
 The shared library is loaded on first use (so that the build step, a submodule of this package, can run
@@ -17,7 +20,9 @@ implementation.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -28,7 +33,8 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqlora_nf4.so")
 
 QLORA_F32, QLORA_BF16 = 0, 1
-STATUS_NONFINITE, STATUS_TIMEOUT = 1, 2
+QLORA_I32, QLORA_I64 = 0, 1
+STATUS_NONFINITE, STATUS_TIMEOUT, STATUS_TARGET = 1, 2, 4
 PROF_NAMES = ("quantize", "dequantize", "fwd_gemm", "bwd_gemm", "lora")
 
 
@@ -36,6 +42,12 @@ class _NF4Struct(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("absmax_e4m3", ctypes.c_void_p),
                 ("scale2", ctypes.c_void_p), ("offset", ctypes.c_void_p),
                 ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
+
+
+class _RopeTensor(ctypes.Structure):
+    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("heads", ctypes.c_int64),
+                ("in_b", ctypes.c_int64), ("in_t", ctypes.c_int64), ("in_h", ctypes.c_int64),
+                ("out_b", ctypes.c_int64), ("out_t", ctypes.c_int64), ("out_h", ctypes.c_int64)]
 
 
 _LIB = None
@@ -83,6 +95,13 @@ def _open() -> ctypes.CDLL:
         "qlora_linear_fwd": [vp, i64, P(_NF4Struct), vp, vp, i32, ctypes.c_float, vp, vp, vp, sz, vp],
         "qlora_linear_bwd": [vp, vp, i64, P(_NF4Struct), vp, vp, i32, ctypes.c_float, vp, vp, vp, vp,
                              vp, sz, vp],
+        "qlora_codebook_linear": [vp, i64, vp, vp, i64, i64, P(ctypes.c_float), i32, vp, vp],
+        "qlora_rope_frequencies": [i32, ctypes.c_double, i32, ctypes.c_double, ctypes.c_double, ctypes.c_double,
+                                   ctypes.c_double, P(ctypes.c_double), P(ctypes.c_double)],
+        "qlora_rope": [P(_RopeTensor), i32, i32, i64, i64, i32, i32, i32, P(ctypes.c_double), ctypes.c_double, vp, i32,
+                       i64, i64, i32, vp],
+        "qlora_vocab_loss_workspace": [i64, i64, i64, i32, P(sz)],
+        "qlora_vocab_loss": [vp, i64, vp, i64, i64, vp, i32, i64, i32, vp, vp, vp, vp, vp, sz, vp],
         "qlora_get_status": [P(i32), vp],
         "qlora_set_wait_limit": [ctypes.c_uint64],
         "qlora_selftest_wait": [i32, vp],
@@ -121,6 +140,17 @@ def _ptr(t) -> ctypes.c_void_p:
 def _need(t: torch.Tensor, dtype, name: str) -> None:
     if not t.is_cuda or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous CUDA tensor of {dtype}, got {t.dtype} on {t.device}")
+
+
+def _on(device: torch.device):
+    """The device made current for a call whose tensors live there."""
+    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def _same_device(device, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
 
 
 # ---- host-only queries --------------------------------------------------------------------------
@@ -324,6 +354,197 @@ def lloyd(w: torch.Tensor, levels, iters: int, stream=None):
     return lv, hist
 
 
+# ---- products of a few tokens with a codebook-quantized weight -------------------------------------------
+
+CODEBOOK_LINEAR_MAX_TOKENS = 64
+
+
+@functools.lru_cache(maxsize=64)
+def _level_array(levels: tuple):
+    return _levels(levels)
+
+
+@functools.lru_cache(maxsize=1)
+def _nf4_levels() -> tuple:
+    return tuple(float(v) for v in codebook()[0])
+
+
+def codebook_linear(X: torch.Tensor, codes: torch.Tensor, absmax: torch.Tensor, N: int, levels,
+                    out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Y = X W^T (T x N bf16) for X (T x K bf16, T <= CODEBOOK_LINEAR_MAX_TOKENS) and the N x K weight that
+    codebook_quantize(w, levels) wrote as codes and absmax (qlora_codebook_linear). K % 64 == 0."""
+    if X.dim() != 2:
+        raise ValueError("codebook_linear: X must be T x K")
+    _need(X, torch.bfloat16, "X")
+    _need(codes, torch.uint8, "codes")
+    _need(absmax, torch.float32, "absmax")
+    T, K = X.shape
+    if codes.numel() != -(-N * K // 2) or absmax.numel() != -(-N * K // 64):
+        raise ValueError(f"codebook_linear: codes / absmax are not those of a {N} x {K} weight")
+    Y = out if out is not None else torch.empty(T, N, dtype=torch.bfloat16, device=X.device)
+    _need(Y, torch.bfloat16, "out")
+    if Y.numel() != T * N:
+        raise ValueError(f"codebook_linear: out must be {T} x {N}")
+    _same_device(X.device, codes=codes, absmax=absmax, out=Y)
+    lv, nl = _level_array(tuple(levels))
+    with _on(X.device):
+        _check(load().qlora_codebook_linear(_ptr(X), T, _ptr(codes), _ptr(absmax), N, K, lv, nl, _ptr(Y),
+                                            _stream(stream)), "qlora_codebook_linear")
+    return Y
+
+
+def linear_single(X: torch.Tensor, q: NF4SingleWeight, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Y = X W^T for a few tokens and a weight of quantize_single (NF4 codes, fp32 block constants)."""
+    if X.dim() != 2 or X.shape[1] != q.cols:
+        raise ValueError(f"linear_single: X must be T x {q.cols}")
+    return codebook_linear(X, q.codes, q.absmax, q.rows, _nf4_levels(), out=out, stream=stream)
+
+
+# ---- rotary positions ------------------------------------------------------------------------------------
+
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "banded": 3, "yarn": 4}
+
+
+@dataclass(frozen=True)
+class RotaryConfig:
+    """Rotary settings of a model (see qlora_rope_frequencies). layout: "half" pairs feature i with
+    i + rotary_dim/2, "interleaved" 2i with 2i + 1. scaling: "none", "linear", "ntk", "banded" or "yarn", by
+    `factor`; "banded" and "yarn" need original_length, the context the model was trained on, and take low /
+    high, in turns over it (defaults: banded 1 and 4, yarn 1 and 32). mscale: None for the scaling's own."""
+    rotary_dim: int
+    base: float = 10000.0
+    layout: str = "half"
+    scaling: str = "none"
+    factor: float = 1.0
+    original_length: float = 0.0
+    low: float | None = None
+    high: float | None = None
+    mscale: float | None = None
+
+    def frequencies(self):
+        """(angle per position of each pair, float64[rotary_dim / 2]; mscale)."""
+        th, m, _ = _rope_setup(self)
+        return np.array(th, np.float64), m
+
+
+@functools.lru_cache(maxsize=64)
+def _rope_setup(c: RotaryConfig):
+    if c.layout not in ROPE_LAYOUTS or c.scaling not in ROPE_SCALINGS:
+        raise ValueError(f"RotaryConfig: unknown layout {c.layout!r} or scaling {c.scaling!r}")
+    low = 1.0 if c.low is None else c.low
+    high = (32.0 if c.scaling == "yarn" else 4.0) if c.high is None else c.high
+    th = (ctypes.c_double * max(1, int(c.rotary_dim) // 2))()
+    m = ctypes.c_double()
+    _check(load().qlora_rope_frequencies(c.rotary_dim, c.base, ROPE_SCALINGS[c.scaling], c.factor, c.original_length,
+                                         low, high, th, ctypes.byref(m)), "qlora_rope_frequencies")
+    return th, m.value if c.mscale is None else float(c.mscale), ROPE_LAYOUTS[c.layout]
+
+
+def _rope_side(x: torch.Tensor, o: torch.Tensor) -> tuple:
+    xs, os_ = x.stride(), o.stride()
+    if x.dim() == 3:
+        return x.data_ptr(), o.data_ptr(), x.shape[1], 0, xs[0], xs[1], 0, os_[0], os_[1]
+    return x.data_ptr(), o.data_ptr(), x.shape[2], xs[0], xs[1], xs[2], os_[0], os_[1], os_[2]
+
+
+def rotary(q: torch.Tensor, k: torch.Tensor | None, config: RotaryConfig, positions: torch.Tensor | None = None,
+           offset: int = 0, inverse: bool = False, out=None, stream=None):
+    """Turn the heads of q and k (fp32 or bf16; (T, heads, dim) or (B, T, heads, dim), any strides with
+    contiguous features) by their tokens' positions, in one launch (qlora_rope); k may be None. positions:
+    int32 or int64, (T,) or (B, T), plus `offset`; without positions token t sits at offset + t. inverse turns
+    back, which is the gradient. out: a pair of tensors like (q, k), the inputs themselves for in place.
+    Returns (q', k')."""
+    if q.dim() not in (3, 4) or q.dtype not in (torch.float32, torch.bfloat16) or not q.is_cuda:
+        raise ValueError("rotary: q must be a (T, heads, dim) or (B, T, heads, dim) CUDA tensor of float32 or bfloat16")
+    lead = q.shape[:-2]
+    if k is not None and (k.dtype != q.dtype or k.shape[:-2] != lead or k.shape[-1] != q.shape[-1]):
+        raise ValueError("rotary: k must match q in type, tokens and head size")
+    qo, ko = (None, None) if out is None else out
+    qo = torch.empty_like(q) if qo is None else qo
+    ko = (torch.empty_like(k) if ko is None else ko) if k is not None else None
+    _same_device(q.device, k=k, out=qo, k_out=ko, positions=positions)
+    for x, o in ((q, qo), (k, ko)):
+        if x is not None and (o.shape != x.shape or o.dtype != x.dtype):
+            raise ValueError("rotary: out must match the inputs")
+        if x is not None and (x.stride(-1) != 1 or o.stride(-1) != 1):
+            raise ValueError("rotary: the features of a head must be contiguous")
+    th, mscale, layout = _rope_setup(config)
+    B, T = lead if len(lead) == 2 else (1, lead[0])
+    pos_b = 0
+    if positions is not None:
+        if positions.dtype not in (torch.int32, torch.int64):
+            raise ValueError("rotary: positions must be int32 or int64")
+        if positions.shape not in ((T,), (B, T)) or (T > 1 and positions.stride(-1) != 1):
+            raise ValueError("rotary: positions must be (T,) or (B, T), contiguous along T")
+        pos_b = positions.stride(0) if positions.dim() == 2 else 0
+    n = 1 if k is None else 2
+    sides = (_RopeTensor * n)(_rope_side(q, qo)) if n == 1 else (_RopeTensor * n)(_rope_side(q, qo), _rope_side(k, ko))
+    with _on(q.device):
+        _check(load().qlora_rope(sides, n, QLORA_F32 if q.dtype == torch.float32 else QLORA_BF16, B, T, q.shape[-1],
+                                 config.rotary_dim, layout, th, mscale, _ptr(positions),
+                                 QLORA_I32 if positions is not None and positions.dtype == torch.int32 else QLORA_I64,
+                                 pos_b, offset, 1 if inverse else 0, _stream(stream)), "qlora_rope")
+    return qo, ko
+
+
+# ---- vocabulary loss ---------------------------------------------------------------------------------------
+
+LOSS_REDUCTIONS = {"none": 0, "sum": 1, "mean": 2}
+
+
+def vocab_loss_workspace_bytes(T: int, V: int, K: int, gradient: bool) -> int:
+    b = ctypes.c_size_t()
+    _check(load().qlora_vocab_loss_workspace(T, V, K, 1 if gradient else 0, ctypes.byref(b)),
+           "qlora_vocab_loss_workspace")
+    return b.value
+
+
+def vocab_loss(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, ignore_index: int = -100,
+               reduction: str = "mean", dloss: torch.Tensor | None = None, need_dx: bool = True,
+               dX: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """Softmax cross entropy of the logits X W^T (X: T x K bf16, W: V x K bf16) with targets (T, int32 or int64),
+    without keeping the logits, and its gradient with respect to X (qlora_vocab_loss). reduction: "mean" over
+    the tokens whose target is not ignore_index, "sum", or "none" (a loss per token, whose gradients `dloss`,
+    fp32, default to ones). Returns (loss fp32, dX bf16 or None); W is frozen and gets no gradient."""
+    if reduction not in LOSS_REDUCTIONS:
+        raise ValueError(f"vocab_loss: unknown reduction {reduction!r}")
+    if dloss is not None and reduction != "none":
+        raise ValueError("vocab_loss: dloss goes with reduction='none'")
+    _need(X, torch.bfloat16, "X")
+    _need(W, torch.bfloat16, "W")
+    if X.dim() != 2 or W.dim() != 2 or X.shape[1] != W.shape[1]:
+        raise ValueError("vocab_loss: X must be T x K and W V x K")
+    T, K = X.shape
+    if targets.dtype not in (torch.int32, torch.int64):
+        raise ValueError("vocab_loss: targets must be int32 or int64")
+    _need(targets, targets.dtype, "targets")
+    if targets.numel() != T:
+        raise ValueError(f"vocab_loss: {T} targets expected, got {targets.numel()}")
+    if dloss is not None:
+        _need(dloss, torch.float32, "dloss")
+        if dloss.numel() != T:
+            raise ValueError(f"vocab_loss: dloss must have {T} elements")
+    dev = X.device
+    dXo = dX if dX is not None else (torch.empty_like(X) if need_dx else None)
+    if dXo is not None:
+        _need(dXo, torch.bfloat16, "dX")
+        if dXo.shape != X.shape:
+            raise ValueError("vocab_loss: dX must be like X")
+    _same_device(dev, W=W, targets=targets, dloss=dloss, dX=dXo, workspace=workspace)
+    ws = workspace if workspace is not None else torch.empty(
+        vocab_loss_workspace_bytes(T, W.shape[0], K, dXo is not None), dtype=torch.uint8, device=dev)
+    red = LOSS_REDUCTIONS[reduction]
+    each = torch.empty(T, dtype=torch.float32, device=dev) if red == 0 else None
+    total = torch.empty((), dtype=torch.float32, device=dev) if red else None
+    with _on(dev):
+        _check(load().qlora_vocab_loss(_ptr(X), T, _ptr(W), W.shape[0], K, _ptr(targets),
+                                       QLORA_I32 if targets.dtype == torch.int32 else QLORA_I64, ignore_index, red,
+                                       _ptr(dloss), _ptr(each), _ptr(total), _ptr(dXo), _ptr(ws), ws.numel(),
+                                       _stream(stream)), "qlora_vocab_loss")
+    return (total if red else each), dXo
+
+
 # ---- paged optimizer: AdamW step and managed-memory buffers ------------------------------------------
 
 def adamw_step(p: torch.Tensor, g: torch.Tensor, m: torch.Tensor, v: torch.Tensor, step: int, lr: float,
@@ -447,7 +668,7 @@ def get_status(stream=None) -> int:
     """Synchronize the stream and return (and clear) the device status bits (STATUS_*)."""
     v = ctypes.c_int()
     rc = load().qlora_get_status(ctypes.byref(v), _stream(stream))
-    if rc not in (0, -6, -7):
+    if rc not in (0, -6, -7, -11):
         _check(rc, "qlora_get_status")
     return v.value
 

@@ -1,5 +1,6 @@
 """PyTorch autograd glue for the QLoRA linear layer: the frozen NF4 weight and the trainable LoRA adapters
-as one torch.autograd.Function and an nn.Module around it.
+as one torch.autograd.Function and an nn.Module around it; and for the two operators beside it in a decoder,
+the rotary positions of queries and keys (`rotary`) and the vocabulary loss (`vocab_loss`).
 
 The adapters are fp32 parameters (the pages keep the adapters in full precision for training: PEFT page,
 zerotofrontier.app/sft/peft, "Paged optimizers, and QLoRA end to end"); each call hands bf16 copies to the
@@ -13,7 +14,9 @@ import math
 
 import torch
 
-from . import NF4Weight, linear_bwd, linear_fwd, quantize
+from . import NF4Weight, RotaryConfig, linear_bwd, linear_fwd, quantize
+from . import rotary as _rotary
+from . import vocab_loss as _vocab_loss
 
 
 class QLoRALinearFn(torch.autograd.Function):
@@ -68,3 +71,63 @@ class QLoRALinear(torch.nn.Module):
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         return QLoRALinearFn.apply(x, self.A, self.B, self.w, self.alpha)
+
+
+class RotaryFn(torch.autograd.Function):
+    """(q', k') of bit_nf4_quantized_14_b200.rotary; the gradients are the same rotations turned back."""
+
+    @staticmethod
+    def forward(ctx, q: torch.Tensor, k: torch.Tensor | None, config: RotaryConfig, positions, offset: int):
+        ctx.save_for_backward(positions)
+        ctx.config, ctx.offset = config, offset
+        return _rotary(q, k, config, positions, offset)
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        (positions,) = ctx.saved_tensors
+        dq, dk = (g if g is None or g.stride(-1) == 1 else g.contiguous() for g in (dq, dk))
+        dq, dk = _rotary(dq, dk, ctx.config, positions, ctx.offset, inverse=True)
+        return dq, dk, None, None, None
+
+
+def rotary(q: torch.Tensor, k: torch.Tensor | None, config: RotaryConfig, positions: torch.Tensor | None = None,
+           offset: int = 0):
+    """Differentiable rotary positions (see bit_nf4_quantized_14_b200.rotary): returns (q', k')."""
+    return RotaryFn.apply(q, k, config, positions, offset)
+
+
+class VocabLossFn(torch.autograd.Function):
+    """Cross entropy of x W^T. A mean or a sum leaves dX with the loss itself, kept until the backward scales it
+    by the gradient of the loss; per-token losses are differentiated in the backward, once their gradients
+    are known (the logits are formed again then)."""
+
+    @staticmethod
+    def forward(ctx, x, head, targets, ignore_index: int, reduction: str):
+        x2 = x.reshape(-1, x.shape[-1]).to(torch.bfloat16).contiguous()
+        need = ctx.needs_input_grad[0] and reduction != "none"
+        loss, dx = _vocab_loss(x2, head, targets.reshape(-1).contiguous(), ignore_index, reduction, need_dx=need)
+        ctx.ignore_index, ctx.reduction, ctx.like = ignore_index, reduction, x.shape
+        if reduction == "none":
+            ctx.save_for_backward(x2, head, targets)
+            return loss.view(targets.shape)
+        ctx.save_for_backward(dx)
+        return loss
+
+    @staticmethod
+    def backward(ctx, dloss):
+        if not ctx.needs_input_grad[0]:
+            return None, None, None, None, None
+        if ctx.reduction == "none":
+            x2, head, targets = ctx.saved_tensors
+            _, dx = _vocab_loss(x2, head, targets.reshape(-1).contiguous(), ctx.ignore_index, "none",
+                                dloss=dloss.reshape(-1).float().contiguous())
+        else:
+            dx = ctx.saved_tensors[0] * dloss        # fp32 product, rounded once more to bf16
+        return dx.view(ctx.like), None, None, None, None
+
+
+def vocab_loss(x: torch.Tensor, head: torch.Tensor, targets: torch.Tensor, ignore_index: int = -100,
+               reduction: str = "mean") -> torch.Tensor:
+    """Differentiable vocabulary loss of hidden states x (..., K) with a frozen bf16 head (V x K) and targets
+    (...): the cross entropy of x head^T without its logits (see bit_nf4_quantized_14_b200.vocab_loss)."""
+    return VocabLossFn.apply(x, head, targets, ignore_index, reduction)

@@ -24,6 +24,9 @@
 #include "gemm_sm100.cuh"
 #include "gemv_nf4.cuh"
 #include "decode_nf4.cuh"
+#include "codebook_linear.cuh"
+#include "rope.cuh"
+#include "vocab_loss.cuh"
 #include "selftest.cuh"
 
 namespace qnf4 {
@@ -824,6 +827,182 @@ int launch_pass1_single(const void* w, int w_dtype, int64_t n, uint8_t* codes, f
 
 static_assert(kStatOut == QLORA_CODEBOOK_STATS_LEN, "codebook statistics layout");
 int64_t stat_ctas(int64_t n) { return std::min<int64_t>(cdiv(cdiv(n, kStepElems), kStatThreads / 32), kStatMaxCtas); }
+// ---- product of a few tokens with a codebook-quantized weight --------------------------------------
+template <int NT>
+int launch_codebook_linear(const ClParams& p, const CodebookArg& cb, int sms, cudaStream_t st) {
+  constexpr int smem = kClTableBytes + kClWarps * 16 * 8 * NT * 4;
+  auto kern = codebook_linear_kernel<NT>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return cuda_fail(cudaGetLastError(), "cudaFuncSetAttribute", __LINE__);
+  kern<<<std::min(p.tiles, sms), kClWarps * 32, smem, st>>>(p, cb);
+  return launched();
+}
+
+// ---- rotary positions ------------------------------------------------------------------------------
+constexpr double kTwoPi = 6.283185307179586476925286766559;
+
+template <typename T, int VE, int AL, bool HALF>
+int launch_rope(RopeParams& p, bool copy_tail, int sms, cudaStream_t st) {
+  p.units = HALF ? p.rotary_dim / (2 * VE) : p.rotary_dim / VE;
+  p.tail = copy_tail ? static_cast<int>(cdiv(p.head_dim - p.rotary_dim, VE)) : 0;
+  const int per_head = p.units + p.tail;
+  p.slots = std::max(1, std::min(kRopeThreads / per_head, p.heads));
+  // four tokens share a CTA's set-up once that still leaves every SM several CTAs; heads are split over CTAs
+  // where there are few tokens
+  const int tok = p.tokens >= int64_t(sms) * 16 ? 4 : 1;
+  const int64_t gx = cdiv(p.tokens, tok);
+  const int64_t want = cdiv(int64_t(sms) * 4, gx), most = cdiv(p.heads, p.slots);
+  const int64_t gy = std::max<int64_t>(1, std::min(want, most));
+  p.heads_per_cta = static_cast<int>(cdiv(cdiv(p.heads, gy), p.slots) * p.slots);
+  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(cdiv(p.heads, p.heads_per_cta)));
+  const unsigned threads = static_cast<unsigned>(per_head * p.slots);
+  const size_t smem = static_cast<size_t>(tok) * p.rotary_dim * 4;
+  if (tok == 4) rope_kernel<T, VE, AL, HALF, 4><<<grid, threads, smem, st>>>(p);
+  else rope_kernel<T, VE, AL, HALF, 1><<<grid, threads, smem, st>>>(p);
+  return launched();
+}
+// The widest access (16 bytes at most) that the sizes and strides allow: `step` divides every offset.
+template <typename T>
+int launch_rope_type(RopeParams& p, bool half, bool copy_tail, int64_t step, int sms, cudaStream_t st) {
+  constexpr int W = 16 / sizeof(T);
+  const int64_t pairs = half ? p.rotary_dim / 2 : p.rotary_dim;
+  auto fits = [&](int ve) { return pairs % ve == 0 && step % ve == 0; };
+  if (half) {
+    if (W == 8 && fits(8)) return launch_rope<T, W, W, true>(p, copy_tail, sms, st);
+    if (fits(4)) return launch_rope<T, 4, 4, true>(p, copy_tail, sms, st);
+    if (fits(2)) return launch_rope<T, 2, 2, true>(p, copy_tail, sms, st);
+    return launch_rope<T, 1, 1, true>(p, copy_tail, sms, st);
+  }
+  if (W == 8 && fits(8)) return launch_rope<T, W, W, false>(p, copy_tail, sms, st);
+  if (fits(4)) return launch_rope<T, 4, 4, false>(p, copy_tail, sms, st);
+  if (fits(2)) return launch_rope<T, 2, 2, false>(p, copy_tail, sms, st);
+  return launch_rope<T, 2, 1, false>(p, copy_tail, sms, st);
+}
+
+// ---- vocabulary loss -------------------------------------------------------------------------------
+constexpr int kVlCtas = 148;                              // one CTA per SM of a B200 (fixed: the plan sizes the workspace)
+constexpr int64_t kVlPieceWords = int64_t(1) << 26;       // token x word weights of one piece (bf16: 128 MB)
+constexpr int64_t kVlPieceRows = 16384;
+
+// How a call is cut up, from its sizes alone, and its workspace (each part 256-byte aligned).
+struct VlPlan {
+  int64_t rows, pitch;        // tokens per piece (a multiple of 128), words per row of the weights
+  int tiles_v, splits, kb_split;
+  size_t count, target, ly, loss, factor, stats, weights, part, total;
+};
+VlPlan vl_plan(int64_t T, int64_t V, int64_t K, bool grad) {
+  VlPlan w{};
+  w.pitch = cdiv(V, 16) * 16;
+  int64_t most = kVlPieceRows;
+  if (grad) most = std::min(most, std::max<int64_t>(kVlM, kVlPieceWords / w.pitch / kVlM * kVlM));
+  w.rows = cdiv(cdiv(T, cdiv(T, most)), kVlM) * kVlM;
+  w.tiles_v = static_cast<int>(cdiv(V, kVlN));
+  // the gradient's tiles, split along the vocabulary while they do not fill one wave (at least 8 steps each)
+  const int64_t tiles = w.rows / kVlM * cdiv(K, kVlN), nkb = cdiv(V, kVlK);
+  const int64_t s = std::max<int64_t>(1, std::min(kVlCtas / tiles, nkb / 8));
+  w.kb_split = static_cast<int>(cdiv(nkb, s));
+  w.splits = static_cast<int>(cdiv(nkb, w.kb_split));
+  size_t at = 0;
+  auto take = [&](size_t bytes) { const size_t p = at; at += align256(bytes); return p; };
+  w.count = take(8);
+  w.target = take(static_cast<size_t>(T) * 8);
+  w.ly = take(static_cast<size_t>(T) * 4);
+  w.loss = take(static_cast<size_t>(T) * 4);
+  w.stats = take(static_cast<size_t>(w.tiles_v) * w.rows * sizeof(float2));
+  if (grad) {
+    w.factor = take(static_cast<size_t>(w.rows) * 4);
+    w.weights = take(static_cast<size_t>(w.rows) * w.pitch * 2);
+    if (w.splits > 1) w.part = take(static_cast<size_t>(w.splits) * w.rows * K * 4);
+  }
+  w.total = at;
+  return w;
+}
+template <bool GRAD>
+int launch_vl_gemm(const CUtensorMap& a, const CUtensorMap& b, const VlParams& p, int sms, cudaStream_t st) {
+  auto kern = vl_gemm_kernel<GRAD>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kVlSmemBytes) != cudaSuccess)
+    return cuda_fail(cudaGetLastError(), "cudaFuncSetAttribute", __LINE__);
+  kern<<<std::min(p.tiles_m * p.tiles_n * p.splits, sms), kVlThreads, kVlSmemBytes, st>>>(a, b, p);
+  return launched();
+}
+bool vl_shape_ok(int64_t T, int64_t V, int64_t K) {
+  return T >= 1 && T <= kMaxTokens && V >= 1 && V < (int64_t(1) << 30) && K >= 8 && K <= (int64_t(1) << 20) &&
+         K % 8 == 0;
+}
+int run_vocab_loss(const __nv_bfloat16* X, int64_t T, const __nv_bfloat16* W, int64_t V, int64_t K, const void* targets,
+                   bool t64, int64_t ignore, int reduction, const float* dloss, float* loss, float* total,
+                   __nv_bfloat16* dX, char* ws, cudaStream_t st) {
+  int sms = 0;
+  if (int e = check_device(&sms)) return e;
+  const VlPlan L = vl_plan(T, V, K, dX != nullptr);
+  auto* count = reinterpret_cast<unsigned long long*>(ws + L.count);
+  auto* target = reinterpret_cast<int64_t*>(ws + L.target);
+  auto* ly = reinterpret_cast<float*>(ws + L.ly);
+  float* tok_loss = loss ? loss : reinterpret_cast<float*>(ws + L.loss);
+  auto* stats = reinterpret_cast<float2*>(ws + L.stats);
+  auto* weights = dX ? reinterpret_cast<__nv_bfloat16*>(ws + L.weights) : nullptr;
+  float* factor = dX ? reinterpret_cast<float*>(ws + L.factor) : nullptr;
+  const int mean = reduction == QLORA_LOSS_MEAN ? 1 : 0;
+  if (cudaMemsetAsync(count, 0, 8, st) != cudaSuccess) return cuda_fail(cudaGetLastError(), "cudaMemsetAsync", __LINE__);
+  const unsigned tg = static_cast<unsigned>(cdiv(T, 8));
+  if (t64)
+    vl_target_kernel<int64_t><<<tg, 256, 0, st>>>(X, W, static_cast<const int64_t*>(targets), T, V, static_cast<int>(K),
+                                                  ignore, target, ly, count);
+  else
+    vl_target_kernel<int32_t><<<tg, 256, 0, st>>>(X, W, static_cast<const int32_t*>(targets), T, V, static_cast<int>(K),
+                                                  ignore, target, ly, count);
+  if (int e = launched()) return e;
+  CUtensorMap tw, tx, twm, tp;
+  if (!tmap_kmajor(&tw, W, K, V, kVlN)) return cuda_fail(cudaGetLastError(), "tensor-map encode", __LINE__);
+  if (dX && !tmap_mnmajor(&twm, W, K, V)) return cuda_fail(cudaGetLastError(), "tensor-map encode", __LINE__);
+  for (int64_t r0 = 0; r0 < T; r0 += L.rows) {
+    const int64_t rows = std::min(L.rows, T - r0);
+    if (!tmap_kmajor(&tx, X + r0 * K, K, rows, kVlM)) return cuda_fail(cudaGetLastError(), "tensor-map encode", __LINE__);
+    VlParams p{};
+    p.rows = static_cast<int>(rows);
+    p.cols = static_cast<int>(V);
+    p.tiles_m = static_cast<int>(cdiv(rows, kVlM));
+    p.tiles_n = L.tiles_v;
+    p.splits = 1;
+    p.nkb = p.kb_split = static_cast<int>(cdiv(K, kVlK));
+    p.target = target + r0;
+    p.ly = ly + r0;
+    p.stats = stats;
+    p.weights = weights;
+    p.pitch = L.pitch;
+    if (int e = launch_vl_gemm<false>(tx, tw, p, sms, st)) return e;
+    vl_finish_kernel<<<static_cast<unsigned>(cdiv(rows, 8)), 256, 0, st>>>(
+        stats, static_cast<int>(rows), L.tiles_v, target + r0, static_cast<int>(V), dloss ? dloss + r0 : nullptr, mean,
+        count, tok_loss + r0, weights, L.pitch, factor);
+    if (int e = launched()) return e;
+    if (!dX) continue;
+    if (!make_tmap_t(&tp, weights, TmType::kBf16, V, rows, L.pitch, kVlK, kVlM, true))
+      return cuda_fail(cudaGetLastError(), "tensor-map encode", __LINE__);
+    VlParams d{};
+    d.rows = static_cast<int>(rows);
+    d.cols = static_cast<int>(K);
+    d.tiles_m = p.tiles_m;
+    d.tiles_n = static_cast<int>(cdiv(K, kVlN));
+    d.splits = L.splits;
+    d.nkb = static_cast<int>(cdiv(V, kVlK));
+    d.kb_split = L.kb_split;
+    d.factor = factor;
+    d.out = dX + r0 * K;
+    d.part = reinterpret_cast<float*>(ws + L.part);
+    if (int e = launch_vl_gemm<true>(tp, twm, d, sms, st)) return e;
+    if (L.splits > 1) {
+      const unsigned grid = static_cast<unsigned>(std::min<int64_t>(cdiv(rows * K / 4, 256), int64_t(sms) * 8));
+      vl_reduce_kernel<<<grid, 256, 0, st>>>(reinterpret_cast<const float4*>(d.part), L.splits, rows, K / 4, factor,
+                                             reinterpret_cast<uint2*>(d.out));
+      if (int e = launched()) return e;
+    }
+  }
+  if (total) {
+    vl_total_kernel<<<1, 1024, 0, st>>>(tok_loss, T, mean, count, total);
+    return launched();
+  }
+  return QLORA_OK;
+}
 }  // namespace
 }  // namespace qnf4
 
@@ -1176,6 +1355,147 @@ int qlora_linear_bwd(const void* dY, const void* X, int64_t T, const qlora_nf4_t
   return QLORA_OK;
 }
 
+int qlora_codebook_linear(const void* X, int64_t T, const void* codes, const float* absmax, int64_t N, int64_t K,
+                          const float* levels, int nlevels, void* Y, qlora_stream_t stream) {
+  if (!X || !codes || !absmax || !Y) return QLORA_ERR_INVALID_ARG;
+  if (T < 1 || T > kClMaxTokens || N < 1 || N > (int64_t(1) << 30) || K < 64 || K > (int64_t(1) << 30) || K % 64 != 0)
+    return QLORA_ERR_SHAPE;
+  CodebookArg cb;
+  BucketArg bk;
+  if (!make_codebook(levels, nlevels, &cb, &bk)) return QLORA_ERR_CODEBOOK;
+  if (!aligned16(X) || !aligned16(codes) || !aligned16(absmax) || !aligned16(Y)) return QLORA_ERR_ALIGNMENT;
+  INJECT("qlora_codebook_linear");
+  int sms = 0;
+  if (int e = check_device(&sms)) return e;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  ClParams p{};
+  p.T = static_cast<int>(T);
+  p.N = static_cast<int>(N);
+  p.nkb = static_cast<int>(K / 64);
+  p.tiles = static_cast<int>(cdiv(N, 16));
+  p.X = static_cast<const __nv_bfloat16*>(X);
+  p.codes = static_cast<const uint8_t*>(codes);
+  p.absmax = absmax;
+  p.Y = static_cast<__nv_bfloat16*>(Y);
+  if (T <= 8) return launch_codebook_linear<1>(p, cb, sms, st);
+  if (T <= 16) return launch_codebook_linear<2>(p, cb, sms, st);
+  if (T <= 32) return launch_codebook_linear<4>(p, cb, sms, st);
+  return launch_codebook_linear<8>(p, cb, sms, st);
+}
+
+int qlora_rope_frequencies(int rotary_dim, double base, int scaling, double factor, double original_length,
+                           double low, double high, double* theta, double* mscale) {
+  if (!theta || !mscale || scaling < QLORA_ROPE_PLAIN || scaling > QLORA_ROPE_YARN) return QLORA_ERR_INVALID_ARG;
+  if (rotary_dim < 2 || rotary_dim > QLORA_ROPE_MAX_DIM || rotary_dim % 2 != 0) return QLORA_ERR_SHAPE;
+  if (!(base > 1.0) || !std::isfinite(base)) return QLORA_ERR_INVALID_ARG;
+  const double R = rotary_dim;
+  if (scaling != QLORA_ROPE_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor))) return QLORA_ERR_INVALID_ARG;
+  if (scaling == QLORA_ROPE_NTK && rotary_dim == 2) return QLORA_ERR_SHAPE;
+  if (scaling >= QLORA_ROPE_BANDED && (!(original_length > 0.0) || !std::isfinite(original_length) || !(low > 0.0) ||
+                                       !(high > low) || !std::isfinite(high)))
+    return QLORA_ERR_INVALID_ARG;
+  const double b = scaling == QLORA_ROPE_NTK ? base * std::pow(factor, R / (R - 2.0)) : base;
+  double lo = 0.0, hi = 0.0;
+  if (scaling == QLORA_ROPE_YARN) {
+    auto dim = [&](double turns) { return R * std::log(original_length / (turns * kTwoPi)) / (2.0 * std::log(base)); };
+    lo = std::min(std::max(std::floor(dim(high)), 0.0), R - 1.0);
+    hi = std::min(std::max(std::ceil(dim(low)), 0.0), R - 1.0);
+    if (!(hi > lo)) hi = lo + 0.001;       // one step instead of a ramp
+  }
+  *mscale = scaling == QLORA_ROPE_YARN && factor > 1.0 ? 0.1 * std::log(factor) + 1.0 : 1.0;
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    const double t = std::pow(b, -2.0 * i / R);
+    double keep = 1.0;                     // how much of the plain angle stays
+    if (scaling == QLORA_ROPE_LINEAR) keep = 0.0;
+    if (scaling == QLORA_ROPE_BANDED) keep = (original_length * t / kTwoPi - low) / (high - low);
+    if (scaling == QLORA_ROPE_YARN) keep = 1.0 - (i - lo) / (hi - lo);
+    keep = std::min(std::max(keep, 0.0), 1.0);
+    theta[i] = keep == 1.0 ? t : (1.0 - keep) * (t / factor) + keep * t;
+  }
+  return QLORA_OK;
+}
+
+int qlora_rope(const qlora_rope_tensor* x, int nx, int dtype, int64_t B, int64_t T, int head_dim, int rotary_dim,
+               int layout, const double* theta, double mscale, const void* positions, int pos_dtype, int64_t pos_b,
+               int64_t pos_offset, int inverse, qlora_stream_t stream) {
+  if (!x || nx < 1 || nx > kRopeMaxTensors || !theta || !std::isfinite(mscale)) return QLORA_ERR_INVALID_ARG;
+  if ((dtype != QLORA_F32 && dtype != QLORA_BF16) || (layout != QLORA_ROPE_HALF && layout != QLORA_ROPE_INTERLEAVED) ||
+      (positions && pos_dtype != QLORA_I32 && pos_dtype != QLORA_I64))
+    return QLORA_ERR_INVALID_ARG;
+  if (B < 1 || T < 1 || B > kMaxNumel || T > kMaxNumel / B || head_dim < 2 || head_dim > QLORA_ROPE_MAX_HEAD ||
+      rotary_dim < 2 || rotary_dim > QLORA_ROPE_MAX_DIM || rotary_dim % 2 != 0 || rotary_dim > head_dim ||
+      B * T > int64_t(INT_MAX))
+    return QLORA_ERR_SHAPE;
+  RopeParams p{};
+  int64_t heads = 0, step = 0;             // step: greatest common divisor of the strides
+  bool in_place = true;
+  auto fold = [&](int64_t s) {
+    int64_t a = s < 0 ? -s : s, b = step;
+    while (b) { const int64_t r = a % b; a = b; b = r; }
+    step = a;
+  };
+  for (int i = 0; i < nx; ++i) {
+    const qlora_rope_tensor& t = x[i];
+    if (!t.in || !t.out) return QLORA_ERR_INVALID_ARG;
+    if (t.heads < 1 || t.heads > 65536) return QLORA_ERR_SHAPE;
+    if (!aligned16(t.in) || !aligned16(t.out)) return QLORA_ERR_ALIGNMENT;
+    p.x[i] = {t.in, t.out, t.in_b, t.in_t, t.in_h, t.out_b, t.out_t, t.out_h};
+    heads += t.heads;
+    if (t.in != t.out || t.in_b != t.out_b || t.in_t != t.out_t || t.in_h != t.out_h) in_place = false;
+    if (B > 1) { fold(t.in_b); fold(t.out_b); }
+    if (T > 1) { fold(t.in_t); fold(t.out_t); }
+    if (t.heads > 1) { fold(t.in_h); fold(t.out_h); }
+  }
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    if (!std::isfinite(theta[i])) return QLORA_ERR_INVALID_ARG;
+    p.turns[i] = theta[i] / kTwoPi;
+  }
+  INJECT("qlora_rope");
+  int sms = 0;
+  if (int e = check_device(&sms)) return e;
+  p.heads0 = static_cast<int>(x[0].heads);
+  p.heads = static_cast<int>(heads);
+  p.T = T;
+  p.tokens = B * T;
+  p.rotary_dim = rotary_dim;
+  p.head_dim = head_dim;
+  p.positions = positions;
+  p.pos64 = pos_dtype == QLORA_I64 ? 1 : 0;
+  p.pos_b = pos_b;
+  p.offset = pos_offset;
+  p.mscale = static_cast<float>(mscale);
+  p.inverse = inverse ? 1 : 0;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool half = layout == QLORA_ROPE_HALF, tail = !in_place && head_dim > rotary_dim;
+  return dtype == QLORA_BF16 ? launch_rope_type<__nv_bfloat16>(p, half, tail, step, sms, st)
+                             : launch_rope_type<float>(p, half, tail, step, sms, st);
+}
+
+int qlora_vocab_loss_workspace(int64_t T, int64_t V, int64_t K, int gradient, size_t* bytes) {
+  if (!bytes) return QLORA_ERR_INVALID_ARG;
+  if (!vl_shape_ok(T, V, K)) return QLORA_ERR_SHAPE;
+  *bytes = vl_plan(T, V, K, gradient != 0).total;
+  return QLORA_OK;
+}
+
+int qlora_vocab_loss(const void* X, int64_t T, const void* W, int64_t V, int64_t K, const void* targets,
+                     int target_dtype, int64_t ignore_index, int reduction, const float* dloss, float* loss,
+                     float* total, void* dX, void* workspace, size_t workspace_bytes, qlora_stream_t stream) {
+  if (!X || !W || !targets || (target_dtype != QLORA_I32 && target_dtype != QLORA_I64)) return QLORA_ERR_INVALID_ARG;
+  if (reduction < QLORA_LOSS_NONE || reduction > QLORA_LOSS_MEAN) return QLORA_ERR_INVALID_ARG;
+  if (reduction == QLORA_LOSS_NONE ? (!loss || total) : (!total || dloss)) return QLORA_ERR_INVALID_ARG;
+  if (!vl_shape_ok(T, V, K)) return QLORA_ERR_SHAPE;
+  if (!aligned16(X) || !aligned16(W) || !aligned16(targets) || !aligned16(dloss) || !aligned16(loss) ||
+      !aligned16(total) || !aligned16(dX) || !aligned16(workspace))
+    return QLORA_ERR_ALIGNMENT;
+  if (!workspace || workspace_bytes < vl_plan(T, V, K, dX != nullptr).total) return QLORA_ERR_WORKSPACE;
+  INJECT("qlora_vocab_loss");
+  return run_vocab_loss(static_cast<const __nv_bfloat16*>(X), T, static_cast<const __nv_bfloat16*>(W), V, K, targets,
+                        target_dtype == QLORA_I64, ignore_index, reduction, dloss, loss, total,
+                        static_cast<__nv_bfloat16*>(dX), static_cast<char*>(workspace),
+                        reinterpret_cast<cudaStream_t>(stream));
+}
+
 int qlora_set_wait_limit(uint64_t ns) {
   if (ns != 0 && (ns < 1000 || ns > kWaitLimitNs)) return QLORA_ERR_INVALID_ARG;
   if (int e = check_device(nullptr)) return e;
@@ -1201,6 +1521,7 @@ int qlora_get_status(int* device_status, qlora_stream_t stream) {
     return cuda_fail(cudaGetLastError(), "CUDA call or tensor-map encode", __LINE__);
   *device_status = static_cast<int>(v);
   if (v & kStatusTimeout) return QLORA_ERR_TIMEOUT;
+  if (v & kStatusTarget) return QLORA_ERR_TARGET;
   if (v & kStatusNonfinite) return QLORA_ERR_NONFINITE;
   return QLORA_OK;
 }
@@ -1218,6 +1539,7 @@ const char* qlora_error_string(int code) {
     case QLORA_ERR_UNSUPPORTED: return "device is not an sm_100 GPU";
     case QLORA_ERR_TOO_LARGE: return "input exceeds the fixed scratch of the no-allocation quantize (2^26 elements)";
     case QLORA_ERR_CODEBOOK: return "codebook not 2..16 ascending levels in [-1, 1], or two thresholds within one bucket";
+    case QLORA_ERR_TARGET: return "a target of the vocabulary loss is outside the vocabulary";
   }
   return "unknown error code";
 }

@@ -51,14 +51,17 @@ enum qlora_status_code {
   QLORA_ERR_TIMEOUT = -7,      /* (status) a kernel's bounded wait gave up; its outputs are invalid */
   QLORA_ERR_UNSUPPORTED = -8,  /* the current device is not an sm_100 (B200-class) GPU             */
   QLORA_ERR_TOO_LARGE = -9,    /* input larger than the fixed scratch of qlora_nf4_quantize_noalloc */
-  QLORA_ERR_CODEBOOK = -10     /* codebook not 2..16 ascending levels in [-1, 1], or too dense      */
+  QLORA_ERR_CODEBOOK = -10,    /* codebook not 2..16 ascending levels in [-1, 1], or too dense      */
+  QLORA_ERR_TARGET = -11       /* (status) a target of qlora_vocab_loss lies outside the vocabulary  */
 };
 
 /* Bits of the device status word (qlora_get_status). */
-enum { QLORA_STATUS_NONFINITE = 1, QLORA_STATUS_TIMEOUT = 2 };
+enum { QLORA_STATUS_NONFINITE = 1, QLORA_STATUS_TIMEOUT = 2, QLORA_STATUS_TARGET = 4 };
 
 /* Element types of quantize inputs and dequantize outputs. */
 enum { QLORA_F32 = 0, QLORA_BF16 = 1 };
+/* Integer types of positions and targets. */
+enum { QLORA_I32 = 0, QLORA_I64 = 1 };
 
 /*
  * An NF4 tensor with double-quantized constants [PEFT "Double quantization"; EXPL "For the curious"].
@@ -280,9 +283,94 @@ int qlora_linear_bwd(const void* dY, const void* X, int64_t T, const qlora_nf4_t
                      qlora_stream_t stream);
 
 /*
+ * The product of a few tokens with a codebook-quantized weight, Y = X W^T (the pages multiply the weight
+ * block by block as it is dequantized [PEFT "Block-wise quantization in one page", "The real way"]; here for
+ * the weights of qlora_nf4_quantize_single and qlora_codebook_quantize):
+ *     W[n][k] = level[code] * absmax[n K/64 + k/64],
+ *   X  T x K bf16;  codes, absmax  the N x K weight as those calls write it;  Y  T x N bf16 (written).
+ * The level is rounded to bf16 and multiplied with X in 16-bit precision with fp32 accumulation; the block
+ * constant multiplies in fp32. absmax must be finite. Rules: 1 <= T <= QLORA_CODEBOOK_LINEAR_MAX_TOKENS (a
+ * longer X: dequantize and multiply), K % 64 == 0 (blocks do not cross rows), N >= 1; levels as in
+ * qlora_codebook_quantize. No workspace. Deterministic.
+ */
+#define QLORA_CODEBOOK_LINEAR_MAX_TOKENS 64
+int qlora_codebook_linear(const void* X, int64_t T, const void* codes, const float* absmax, int64_t N,
+                          int64_t K, const float* levels, int nlevels, void* Y, qlora_stream_t stream);
+
+/*
+ * Rotary positions for the query and key heads of a decoder around these linears (not on the pages, whose
+ * models use them; Su et al. 2021). The pair of features (a, b) number i of the first rotary_dim features
+ * of every head is turned by the angle p theta[i] of its token's position p and scaled by mscale:
+ *     a' = mscale (a cos - b sin),  b' = mscale (b cos + a sin);
+ * pairs are (i, i + rotary_dim/2) for QLORA_ROPE_HALF and (2i, 2i + 1) for QLORA_ROPE_INTERLEAVED; the other
+ * features pass through. inverse != 0 turns by -p theta, which is the gradient of the forward.
+ *
+ * qlora_rope_frequencies writes the rotary_dim/2 angles per position (host) and the scale. Plain:
+ * theta_i = base^(-2i/R), R = rotary_dim, mscale 1. For contexts longer than a model was trained on:
+ *   LINEAR  theta_i / factor
+ *   NTK     base * factor^(R/(R-2)) in place of base
+ *   BANDED  turns_i = original_length theta_i / 2 pi; theta_i where turns_i >= high, theta_i / factor where
+ *           turns_i <= low, between them mixed linearly in turns_i
+ *   YARN    theta_i / factor x ramp + theta_i x (1 - ramp), ramp rising linearly in i from 0 at
+ *           floor(d(high)) to 1 at ceil(d(low)), d(b) = R ln(original_length / 2 pi b) / (2 ln base), both
+ *           clamped to [0, R-1]; mscale = 0.1 ln(factor) + 1 for factor > 1 (Peng et al. 2023)
+ * R even, 2 <= R <= QLORA_ROPE_MAX_DIM; base > 1; factor >= 1; BANDED and YARN: original_length > 0 and
+ * 0 < low < high; NTK: R > 2. QLORA_ERR_INVALID_ARG / QLORA_ERR_SHAPE (R) otherwise. Needs no GPU.
+ *
+ * qlora_rope turns nx tensors (1 or 2: queries and keys) of element type `dtype` in one launch. Tensor i has
+ * heads[i] heads of head_dim contiguous features; element (b, t, h, f) of `in` is at
+ * b in_b + t in_t + h in_h + f (strides in elements, any order; likewise `out`). `out` is either exactly
+ * `in` with the same strides (in place) or memory that does not overlap it.
+ * Position of token t of row b: positions[b pos_b + t] + pos_offset (device, QLORA_I32 or QLORA_I64), or
+ * pos_offset + t where positions is NULL. Angles are formed in fp64; the rest is fp32, rounded once.
+ * Rules: B, T, heads >= 1; rotary_dim <= head_dim <= QLORA_ROPE_MAX_HEAD; theta (host) finite.
+ */
+#define QLORA_ROPE_MAX_DIM 512
+#define QLORA_ROPE_MAX_HEAD 1024
+enum { QLORA_ROPE_HALF = 0, QLORA_ROPE_INTERLEAVED = 1 };
+enum { QLORA_ROPE_PLAIN = 0, QLORA_ROPE_LINEAR = 1, QLORA_ROPE_NTK = 2, QLORA_ROPE_BANDED = 3, QLORA_ROPE_YARN = 4 };
+typedef struct qlora_rope_tensor {
+  const void* in;
+  void* out;
+  int64_t heads;
+  int64_t in_b, in_t, in_h;
+  int64_t out_b, out_t, out_h;
+} qlora_rope_tensor;
+int qlora_rope_frequencies(int rotary_dim, double base, int scaling, double factor, double original_length,
+                           double low, double high, double* theta, double* mscale);
+int qlora_rope(const qlora_rope_tensor* x, int nx, int dtype, int64_t B, int64_t T, int head_dim, int rotary_dim,
+               int layout, const double* theta, double mscale, const void* positions, int pos_dtype,
+               int64_t pos_b, int64_t pos_offset, int inverse, qlora_stream_t stream);
+
+/*
+ * Softmax cross entropy over the vocabulary with the output head's product inside, and the gradient with
+ * respect to the hidden states; the T x V logits are never kept (the head is frozen like every base weight
+ * [EXPL "Putting it together"], so it gets no gradient):
+ *     l = X W^T,   loss_t = log sum_v exp(l_tv) - l_t,y(t),   dX_t = g_t (softmax(l_t) W - W_y(t)).
+ *   X  T x K bf16   W  V x K bf16   targets  T of QLORA_I32 or QLORA_I64 (device)
+ *   loss   T fp32, each token's loss (0 where the target is ignore_index), or NULL
+ *   total  1 fp32: QLORA_LOSS_SUM the sum of loss, QLORA_LOSS_MEAN that over the number of tokens whose
+ *          target is not ignore_index (NaN when there is none); NULL for QLORA_LOSS_NONE
+ *   dloss  T fp32 or NULL (ones): the gradient g_t of each token's loss; QLORA_LOSS_NONE only. For SUM g = 1,
+ *          for MEAN g = 1 / count.
+ *   dX     T x K bf16 (written; zero rows for ignored tokens), or NULL: loss only
+ * A target that is neither ignore_index nor in [0, V) sets QLORA_STATUS_TARGET; its token is then treated
+ * as ignored. fp32 logits and sums; the softmax weights are rounded to bf16 for the gradient's product.
+ * Rules: T, V >= 1 (V < 2^30), K % 8 == 0, 8 <= K <= 2^20. `workspace` >= qlora_vocab_loss_workspace(T, V, K,
+ * dX != NULL), at most about 128 MB for the weights of one piece of the tokens plus 2 K/V of that for the
+ * partial sums of short inputs and 16 bytes per token. Deterministic.
+ */
+enum { QLORA_LOSS_NONE = 0, QLORA_LOSS_SUM = 1, QLORA_LOSS_MEAN = 2 };
+int qlora_vocab_loss_workspace(int64_t T, int64_t V, int64_t K, int gradient, size_t* bytes);
+int qlora_vocab_loss(const void* X, int64_t T, const void* W, int64_t V, int64_t K, const void* targets,
+                     int target_dtype, int64_t ignore_index, int reduction, const float* dloss, float* loss,
+                     float* total, void* dX, void* workspace, size_t workspace_bytes, qlora_stream_t stream);
+
+/*
  * Synchronize `stream`, then read and clear the current device's status word into *device_status
  * (host; a bitwise OR of QLORA_STATUS_* set by kernels since the last call). Returns QLORA_OK, or
- * QLORA_ERR_NONFINITE / QLORA_ERR_TIMEOUT when the corresponding bit was set (TIMEOUT wins).
+ * QLORA_ERR_NONFINITE / QLORA_ERR_TARGET / QLORA_ERR_TIMEOUT when the corresponding bit was set (TIMEOUT
+ * wins, then TARGET).
  */
 int qlora_get_status(int* device_status, qlora_stream_t stream);
 

@@ -1,0 +1,244 @@
+"""The vocabulary loss and its gradient on the GPU against the 64-bit form, element by element.
+
+Tolerances, counted in roundings. A logit: K/16 tensor-core steps, each a truncation of at most 2^-23 of what it
+holds (at most S = sum |x w|), and 16 more for the additions inside a step: e = (K/16 + 16) 2^-23 S. The loss is
+a mean of logits against the target's, so it is off by at most e (largest over the words) plus the target's own
+(32 additions after K/32 in a lane: less than e), plus a few steps of the exponentials (2^-21 (1 + |d|)) and of
+itself. The gradient: each weight p_v is off by that relatively and by half a bf16 step (2^-8), the sum over the
+words by (V/16 + 16) 2^-23 of sum p |W|, the result by half a bf16 step. fp32 and bf16 end at 2^-126: a weight
+below it may be lost whole, so V words can lose V 2^-126 of the loss and V 2^-126 max |W| of a gradient.
+"""
+import pytest
+import torch
+
+from oracle import decoder_ops as R64
+
+pytestmark = pytest.mark.gpu
+
+
+def case(T, V, K, seed=0, lean=0.3, scale=1.0):
+    g = torch.Generator("cuda").manual_seed(seed)
+    W = (torch.randn(V, K, device="cuda", generator=g) * 0.1).bfloat16()
+    y = torch.randint(0, V, (T,), device="cuda", generator=g)
+    X = (scale * (torch.randn(T, K, device="cuda", generator=g) + lean * W[y].float() / 0.1)).bfloat16()
+    return X, W, y
+
+
+def tolerances(X, W, y, g, ignore=-100):
+    X64, W64 = X.double(), W.double()
+    V, K = W.shape
+    at = torch.where(y != ignore, y, 0).long()
+    l = X64 @ W64.t()
+    S = X64.abs() @ W64.abs().t()
+    d = (l - l.gather(1, at[:, None])).abs()
+    e = ((K / 16 + 16) * 2.0 ** -23 * S + 2.0 ** -21 * (1 + d)).amax(1) * 2 + 2.0 ** -20
+    loss, _ = R64.vocab_loss(X, W, y, ignore=ignore)
+    # d loss = sum p (d l_v - d l_y): nothing of it where the target has all of the probability
+    rest = -torch.expm1(-loss)
+    tl = e * (rest + e).clamp(max=1.0) + 2.0 ** -22 * loss + V * 2.0 ** -126
+    p = torch.softmax(l, 1)
+    p.scatter_(1, at[:, None], rest[:, None])
+    mass = p @ W64.abs()
+    tx = mass * ((2.0 ** -8 + 2 * e) * 1.01 + (V / 16 + 16) * 2.0 ** -23)[:, None] + V * 2.0 ** -126 * W64.abs().max()
+    return tl, tx * g.double().abs()[:, None] + 2.0 ** -126
+
+
+def check(lib, X, W, y, g=None, ignore=-100, **kw):
+    ones = torch.ones(X.shape[0], device="cuda") if g is None else g
+    with torch.no_grad():
+        ref, dref = R64.vocab_loss(X, W, y, g, ignore)
+        used = y != ignore
+        X0 = torch.where(used[:, None], X, 0)
+        tl, tx = tolerances(X0, W, y, ones, ignore)
+        loss, dX = lib.vocab_loss(X, W, y, ignore_index=ignore, reduction="none", dloss=g, **kw)
+        assert lib.get_status() == 0
+        off = (loss.double() - ref).abs()
+        assert bool((off <= tl).all()), (float((off - tl).max()), int((off - tl).argmax()))
+        off = (dX.double() - dref).abs()
+        lim = tx + (dref.abs() + tx) * 2.0 ** -8
+        assert bool((off <= lim).all()), (float((off - lim).max()), float((off / lim.clamp_min(1e-300)).max()))
+        # the loss alone is the same loss, bit for bit
+        alone, none = lib.vocab_loss(X, W, y, ignore_index=ignore, reduction="none", need_dx=False)
+        assert none is None and torch.equal(alone, loss)
+    return loss, dX
+
+
+@pytest.mark.parametrize("T,V,K", [(1, 1, 8), (1, 2, 64), (3, 17, 72), (5, 255, 8), (127, 256, 136), (128, 257, 64),
+                                   (129, 1000, 264), (300, 511, 520), (1, 32000, 256), (257, 5003, 64)])
+def test_sizes(lib, T, V, K):
+    check(lib, *case(T, V, K))
+
+
+def test_token_gradients_and_ignored_tokens(lib):
+    X, W, y = case(200, 700, 96, seed=1)
+    y[::3] = -100
+    X[3] = float("nan")                                   # what stands in an ignored token does not matter
+    g = torch.randn(200, device="cuda", generator=torch.Generator("cuda").manual_seed(9))
+    loss, dX = check(lib, X, W, y, g)
+    assert bool((loss[::3] == 0).all()) and bool((dX[::3] == 0).all())
+    check(lib, X, W, torch.where(y < 0, 5, y).int(), ignore=5)    # int32 targets, another index left out
+
+
+def test_all_tokens_ignored(lib):
+    X, W, _ = case(70, 300, 64)
+    y = torch.full((70,), -100, device="cuda")
+    loss, dX = lib.vocab_loss(X, W, y)
+    assert torch.isnan(loss) and bool((dX == 0).all())
+    loss, dX = lib.vocab_loss(X, W, y, reduction="sum")
+    assert float(loss) == 0.0 and bool((dX == 0).all()) and lib.get_status() == 0
+
+
+def test_far_apart_logits(lib):
+    """Targets hundreds below the best word (every tile has a shift, and different ones), hundreds above it, and
+    rows of both kinds in one tile; equal logits."""
+    X, W, y = case(140, 1500, 64, seed=2, lean=0.0, scale=60.0)
+    X[::2] = case(140, 1500, 64, seed=2, lean=3.0, scale=40.0)[0][::2]
+    loss, dX = check(lib, X, W, y)
+    assert float(loss[1::2].max()) > 88 and float(loss[::2].min()) == 0.0
+    assert bool(torch.isfinite(dX.float()).all())
+    X.zero_()
+    loss, _ = check(lib, X, W, y)
+
+
+def test_reductions_and_pieces(lib):
+    """More tokens than one piece of the workspace takes (a large vocabulary), reduced in the call."""
+    X, W, y = case(1100, 131072, 64, seed=3)
+    y[::7] = -100
+    ref, _ = R64.vocab_loss(X, W, y)
+    n = int((y != -100).sum())
+    g = (y != -100).float() / n
+    each, dX = check(lib, X, W, y, g)
+    mean, dmean = lib.vocab_loss(X, W, y)
+    total, dsum = lib.vocab_loss(X, W, y, reduction="sum")
+    # the sum of the tokens' fp32 losses in fp64, rounded once
+    assert abs(float(mean) - float(each.double().sum()) / n) <= 2.0 ** -23 * float(mean)
+    assert abs(float(total) - float(each.double().sum())) <= 2.0 ** -23 * float(total)
+    assert abs(float(mean) - float(ref.sum()) / n) <= 1e-4 * float(mean)
+    _, dones = lib.vocab_loss(X, W, y, reduction="none")
+    assert torch.equal(dsum, dones)
+    d = (dmean.double() - dX.double()).abs()              # g = 1 / n formed in one division either way
+    assert bool((d <= 2.0 ** -7 * dX.double().abs()).all())
+
+
+def test_split_vocabulary_is_deterministic(lib):
+    """A few tokens and features: the gradient's vocabulary is split over the SMs."""
+    X, W, y = case(4, 9000, 128, seed=4)
+    a = check(lib, X, W, y)
+    b = lib.vocab_loss(X, W, y, reduction="none")
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_targets_outside_the_vocabulary(lib):
+    X, W, y = case(130, 300, 64, seed=5)
+    bad = y.clone()
+    bad[7], bad[9], bad[128] = 300, -1, 1 << 40
+    loss, dX = lib.vocab_loss(X, W, bad, reduction="none")
+    assert lib.get_status() == lib.STATUS_TARGET and lib.get_status() == 0
+    rows = [7, 9, 128]
+    assert bool((loss[rows] == 0).all()) and bool((dX[rows] == 0).all())
+    keep = torch.ones(130, dtype=torch.bool, device="cuda")
+    keep[rows] = False
+    ok, dok = lib.vocab_loss(X, W, y, reduction="none")
+    assert torch.equal(loss[keep], ok[keep]) and torch.equal(dX[keep], dok[keep])
+
+
+def test_guards_around_every_output_and_the_workspace(lib):
+    T, V, K = 131, 777, 72
+    X, W, y = case(T, V, K, seed=6)
+    need = lib.vocab_loss_workspace_bytes(T, V, K, True)
+    ws = torch.full((need + 8192,), 0xA5, dtype=torch.uint8, device="cuda")
+    buf = torch.full((T * K + 4096,), 7.0, dtype=torch.bfloat16, device="cuda")
+    dX = buf[2048:2048 + T * K].view(T, K)
+    loss, _ = lib.vocab_loss(X, W, y, reduction="none", dX=dX, workspace=ws[4096:4096 + need])
+    ref, dref = lib.vocab_loss(X, W, y, reduction="none")
+    assert torch.equal(loss, ref) and torch.equal(dX, dref)
+    assert bool((ws[:4096] == 0xA5).all()) and bool((ws[4096 + need:] == 0xA5).all())
+    assert bool((buf[:2048] == 7).all()) and bool((buf[2048 + T * K:] == 7).all())
+
+
+def test_autograd(lib):
+    from bit_nf4_quantized_14_b200.autograd import vocab_loss
+    X, W, y = case(150, 600, 64, seed=7)
+    y[5] = -100
+    for red in ("mean", "sum"):
+        x = X.view(3, 50, 64).clone().requires_grad_()
+        loss = vocab_loss(x, W, y.view(3, 50), reduction=red)
+        (3.0 * loss).backward()
+        ref, dref = lib.vocab_loss(X, W, y, reduction=red)
+        assert torch.equal(loss.detach(), ref)
+        lim = 2.0 ** -8 * (3 * dref.double()).abs()       # one more rounding to bf16
+        assert bool(((x.grad.view(150, 64).double() - 3 * dref.double()).abs() <= lim).all())
+    x = X.clone().requires_grad_()
+    g = torch.rand(150, device="cuda")
+    vocab_loss(x, W, y, reduction="none").backward(g)
+    assert torch.equal(x.grad, lib.vocab_loss(X, W, y, reduction="none", dloss=g)[1])
+    with torch.no_grad():
+        assert vocab_loss(X, W, y).requires_grad is False
+
+
+def test_gradient_against_differences(lib):
+    """Along one direction, a step of the fp32 loss itself (64-bit logits of the moved input are not needed: the
+    sum of 20 tokens' losses moves by 1e-1 and is good to 1e-4)."""
+    X, W, y = case(20, 400, 64, seed=8)
+    g = torch.Generator("cuda").manual_seed(1)
+    d = torch.randn(20, 64, device="cuda", generator=g)
+    up, dn = ((X.float() + s * 0.0625 * d).bfloat16() for s in (1, -1))
+    moved = up.double() - dn.double()
+    _, dX = lib.vocab_loss(X, W, y, reduction="sum")
+    diff = lib.vocab_loss(up, W, y, reduction="sum", need_dx=False)[0] - lib.vocab_loss(dn, W, y, reduction="sum", need_dx=False)[0]
+    ref = R64.vocab_loss(up, W, y)[0].sum() - R64.vocab_loss(dn, W, y)[0].sum()
+    lin = (R64.vocab_loss(X, W, y)[1] * moved).sum()
+    assert abs(float(diff) - float(ref)) < 1e-3
+    # the gradient predicts the step as well as the exact one does, up to its bf16 roundings
+    assert abs(float((dX.double() * moved).sum()) - float(lin)) <= 2.0 ** -6 * float((dX.double() * moved).abs().sum())
+    assert abs(float(lin) - float(ref)) <= 0.05 * abs(float(ref)) + 0.05
+
+
+def test_capture_streams_and_two_calls_at_once(lib):
+    X, W, y = case(160, 900, 128, seed=9)
+    X2, _, y2 = case(160, 900, 128, seed=10)
+    ref, dref = lib.vocab_loss(X, W, y)
+    ref2, dref2 = lib.vocab_loss(X2, W, y2)
+    need = lib.vocab_loss_workspace_bytes(160, 900, 128, True)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    x, t, dX = X.clone(), y.clone(), torch.empty_like(X)
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        loss, _ = lib.vocab_loss(x, W, t, dX=dX, workspace=ws)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(loss, ref) and torch.equal(dX, dref)
+    x.copy_(X2)
+    t.copy_(y2)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(loss, ref2) and torch.equal(dX, dref2)
+    # two streams, workspaces of their own
+    s = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for st, (a, b) in zip(s, ((X, y), (X2, y2))):
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(st):
+            got.append(lib.vocab_loss(a, W, b))
+    torch.cuda.synchronize()
+    assert torch.equal(got[0][1], dref) and torch.equal(got[1][1], dref2) and lib.get_status() == 0
+
+
+def test_refusals(lib):
+    X, W, y = case(8, 64, 64)
+    for bad in (dict(X=X.float()), dict(X=X[:, :32]), dict(W=W.half()), dict(targets=y.float()), dict(targets=y[:4]),
+                dict(reduction="max"), dict(dloss=torch.ones(8, device="cuda")),
+                dict(reduction="none", dloss=torch.ones(7, device="cuda")), dict(targets=y.cpu()), dict(X=X.cpu()),
+                dict(dX=torch.empty(8, 32, device="cuda", dtype=torch.bfloat16))):
+        a = dict(X=X, W=W, targets=y)
+        a.update(bad)
+        with pytest.raises(ValueError):
+            lib.vocab_loss(**a)
+    with pytest.raises(lib.QLoRAError) as e:
+        lib.vocab_loss(X, W, y, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    assert e.value.code == -4
+    with pytest.raises(lib.QLoRAError) as e:
+        lib.vocab_loss(X[:, :60].contiguous(), W[:, :60].contiguous(), y)
+    assert e.value.code == -2
