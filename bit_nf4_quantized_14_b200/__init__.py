@@ -129,8 +129,9 @@ def _check(rc: int, where: str) -> None:
 
 
 def _stream(stream) -> ctypes.c_void_p:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:      # the current stream's handle, without building a Stream object around it
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
+    return ctypes.c_void_p(stream.cuda_stream)
 
 
 def _ptr(t) -> ctypes.c_void_p:
@@ -142,9 +143,12 @@ def _need(t: torch.Tensor, dtype, name: str) -> None:
         raise ValueError(f"{name}: expected a contiguous CUDA tensor of {dtype}, got {t.dtype} on {t.device}")
 
 
+_HERE_ALREADY = contextlib.nullcontext()
+
+
 def _on(device: torch.device):
     """The device made current for a call whose tensors live there."""
-    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    return _HERE_ALREADY if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
 
 
 def _same_device(device, **tensors) -> None:

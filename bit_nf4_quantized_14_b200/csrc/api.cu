@@ -829,12 +829,13 @@ static_assert(kStatOut == QLORA_CODEBOOK_STATS_LEN, "codebook statistics layout"
 int64_t stat_ctas(int64_t n) { return std::min<int64_t>(cdiv(cdiv(n, kStepElems), kStatThreads / 32), kStatMaxCtas); }
 // ---- product of a few tokens with a codebook-quantized weight --------------------------------------
 template <int NT>
-int launch_codebook_linear(const ClParams& p, const CodebookArg& cb, int sms, cudaStream_t st) {
-  constexpr int smem = kClTableBytes + kClWarps * 16 * 8 * NT * 4;
+int launch_codebook_linear(ClParams p, const CodebookArg& cb, int sms, cudaStream_t st) {
   auto kern = codebook_linear_kernel<NT>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, cl_smem_bytes(NT)) != cudaSuccess)
     return cuda_fail(cudaGetLastError(), "cudaFuncSetAttribute", __LINE__);
-  kern<<<std::min(p.tiles, sms), kClWarps * 32, smem, st>>>(p, cb);
+  p.pairs = std::max(1, std::min(p.tiles, sms / 2));
+  const dim3 grid(2u * p.pairs, static_cast<unsigned>(cdiv(p.T, 8 * NT)));
+  kern<<<grid, kClWarps * 32, cl_smem_bytes(NT), st>>>(p, cb);
   return launched();
 }
 
@@ -1379,8 +1380,7 @@ int qlora_codebook_linear(const void* X, int64_t T, const void* codes, const flo
   p.Y = static_cast<__nv_bfloat16*>(Y);
   if (T <= 8) return launch_codebook_linear<1>(p, cb, sms, st);
   if (T <= 16) return launch_codebook_linear<2>(p, cb, sms, st);
-  if (T <= 32) return launch_codebook_linear<4>(p, cb, sms, st);
-  return launch_codebook_linear<8>(p, cb, sms, st);
+  return launch_codebook_linear<4>(p, cb, sms, st);   // above 32: two groups of tokens, the second's weights from L2
 }
 
 int qlora_rope_frequencies(int rotary_dim, double base, int scaling, double factor, double original_length,

@@ -7,9 +7,11 @@
 // a 256-entry table, one copy per lane so the lookups have no bank conflicts. Inside a block of 64 the MMA's k
 // index is permuted alike on both operands, so lane j of a quad holds elements 16 j .. 16 j + 15: 8 code bytes and
 // 32 bytes of X in a row. The block's constant multiplies the fp32 result of its four MMAs, so the only rounding
-// of a weight is its level's to bf16 (a relative 2^-9), as in the T <= 16 forward of the double-quantized layer.
-// The warps of a CTA share a tile of 16 rows and split the contraction; their fp32 sums meet in shared memory and
-// are added in warp order, so results are deterministic.
+// of a weight is its level's to bf16 (a relative 2^-8 at most), as in the T <= 16 forward of the double-quantized layer.
+// Warps run without barriers: a pair of CTAs (a cluster, each CTA with half of the contraction: the finer cut
+// fills 148 SMs evenly) owns a run of row tiles, cut evenly over its warps wherever a tile ends, and each lane
+// keeps the codes and constants of 8 blocks in flight (64 KB per SM). Where a warp leaves a row tile its fp32
+// sums go to shared memory, and at the end of a pass they are added in a fixed order: deterministic.
 #pragma once
 
 #include "codec.cuh"
@@ -20,85 +22,213 @@ namespace qnf4 {
 
 constexpr int kClWarps = 16;
 constexpr int kClMaxTokens = 64;
-constexpr int kClTableBytes = 256 * 32 * 4;
+constexpr int kClDepth = 8;              // blocks of 64 whose codes and constants each lane holds in flight
+// Shared memory: a CTA pair's second half hands its sums over below the table; the table (256 entries of 256
+// bytes, the lane copies in the first 128) sits at shared address 64 KB, so one byte permute forms a lookup's
+// address; the warps' sums of a pass lie above it.
+constexpr uint32_t kClTable = 1u << 16, kClRed = 2u << 16;
+constexpr int kClBaseMax = 4096;         // where the dynamic shared memory may begin, at most
+__host__ __device__ constexpr int cl_pass_tiles(int NT) { return NT <= 2 ? 32 : 16; }
+__host__ __device__ constexpr int cl_segments(int NT) { return cl_pass_tiles(NT) / kClWarps + 2; }   // row tiles one warp may touch in a pass
+__host__ __device__ constexpr int cl_red_bytes(int NT) { return kClWarps * cl_segments(NT) * 16 * 8 * NT * 4; }
+__host__ __device__ constexpr int cl_smem_bytes(int NT) { return static_cast<int>(kClRed) + cl_red_bytes(NT); }
+static_assert(cl_smem_bytes(1) <= 227 * 1024 && cl_smem_bytes(2) <= 227 * 1024 && cl_smem_bytes(4) <= 227 * 1024,
+              "shared memory per CTA");
+static_assert(kClBaseMax + cl_pass_tiles(2) * 16 * 16 * 4 <= 65536 && cl_pass_tiles(4) * 16 * 32 * 4 + kClBaseMax <= 65536,
+              "the handed-over sums lie below the table");
 
 struct ClParams {
-  int T, N, nkb, tiles;
+  int T, N, nkb, tiles, pairs;           // pairs: CTA pairs per token group
   const __nv_bfloat16* X;
   const uint8_t* codes;
   const float* absmax;
   __nv_bfloat16* Y;
 };
 
-template <int NT>   // token tiles of 8
-__global__ void __launch_bounds__(kClWarps * 32, 1) codebook_linear_kernel(const ClParams p, const CodebookArg cb) {
-  extern __shared__ __align__(16) uint8_t cl_smem[];
-  uint32_t* table = reinterpret_cast<uint32_t*>(cl_smem);
-  float* red = reinterpret_cast<float*>(cl_smem + kClTableBytes);   // [warp][16 rows][8 NT tokens]
+// Codes are read once: not kept in L1, and fetched from HBM in runs of 256 bytes of a row.
+__device__ __forceinline__ uint2 cl_ld_codes(const uint8_t* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float cl_ld_scale(const float* p) {
+  float v;
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ void cl_cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Store to the same shared address in CTA `rank` of the cluster.
+__device__ __forceinline__ void cl_st_peer(uint32_t addr, uint32_t rank, float v) {
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\tst.shared::cluster.f32 [a], %2;\n\t}" ::"r"(addr),
+      "r"(rank), "f"(v)
+      : "memory");
+}
+__device__ __forceinline__ float cl_lds(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cl_sts2(uint32_t addr, float a, float b) {
+  asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(a), "f"(b) : "memory");
+}
+
+template <int NT>   // token tiles of 8; blockIdx.y: groups of 8 NT tokens
+__global__ void __launch_bounds__(kClWarps * 32, 1) __cluster_dims__(2, 1, 1)
+    codebook_linear_kernel(const __grid_constant__ ClParams p, const __grid_constant__ CodebookArg cb) {
+  constexpr int PT = cl_pass_tiles(NT), SEG = cl_segments(NT), TT = 8 * NT, D = kClDepth;
+  extern __shared__ __align__(1024) uint8_t cl_smem[];
+  // a CTA's shared addresses lie in its own window of the cluster's: the layout's are relative to that
+  const uint32_t base = smem_u32(cl_smem), window = base & 0xFF000000u;
+  const uint32_t table = window | kClTable, redu = window | kClRed;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, j = lane & 3;
-  for (int i = threadIdx.x; i < 256 * 32; i += blockDim.x)
-    table[i] = pack_bf16x2(cb.levels[i >> 9], cb.levels[(i >> 5) & 15]);
-  __syncthreads();
-  const uint32_t tab = smem_u32(table) + 4u * lane;
+  const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1;
+  const int tok0 = blockIdx.y * TT, T = min(TT, p.T - tok0);
+  const __nv_bfloat16* X = p.X + static_cast<int64_t>(tok0) * p.nkb * 64;
+  if (base - window > kClBaseMax) {      // the table's address needs a low base; the same in both CTAs of the pair
+    if (threadIdx.x == 0) raise_status(kStatusTimeout);
+    return;
+  }
+  for (int i = threadIdx.x; i < 256 * 32; i += blockDim.x) {
+    const uint32_t v = pack_bf16x2(cb.levels[i >> 9], cb.levels[(i >> 5) & 15]);
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(table + (static_cast<uint32_t>(i >> 5) << 8) + 4u * (i & 31)), "r"(v)
+                 : "memory");
+  }
+  cl_cluster_sync();                     // the table is complete; the other CTA of the pair runs
+  const uint32_t lanebyte = table | (4u * lane);
   const int K = p.nkb * 64;
+  const int64_t row_bytes = K / 2;
 
-  for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
-    const int64_t r0 = min(tile * 16 + g, p.N - 1), r1 = min(tile * 16 + g + 8, p.N - 1);
-    const uint8_t* c0 = p.codes + r0 * (K / 2) + 8 * j;
-    const uint8_t* c1 = p.codes + r1 * (K / 2) + 8 * j;
-    const float* a0 = p.absmax + r0 * p.nkb;
-    const float* a1 = p.absmax + r1 * p.nkb;
-    float acc[NT][4] = {};
-#pragma unroll 4
-    for (int kb = warp; kb < p.nkb; kb += kClWarps) {
-      const uint2 w0 = *reinterpret_cast<const uint2*>(c0 + 32 * kb), w1 = *reinterpret_cast<const uint2*>(c1 + 32 * kb);
-      const float s0 = a0[kb], s1 = a1[kb];
-      uint32_t a[16];
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const uint32_t x0 = (s < 2 ? w0.x : w0.y) >> (16 * (s & 1)), x1 = (s < 2 ? w1.x : w1.y) >> (16 * (s & 1));
-        a[4 * s] = dc_lut(tab + ((x0 & 255u) << 7));
-        a[4 * s + 1] = dc_lut(tab + ((x1 & 255u) << 7));
-        a[4 * s + 2] = dc_lut(tab + (((x0 >> 8) & 255u) << 7));
-        a[4 * s + 3] = dc_lut(tab + (((x1 >> 8) & 255u) << 7));
-      }
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-        if (8 * n + g < p.T) {
-          const uint4* xp = reinterpret_cast<const uint4*>(p.X + static_cast<int64_t>(8 * n + g) * K + 64 * kb + 16 * j);
-          x[0] = __ldg(xp);
-          x[1] = __ldg(xp + 1);
+  // this pair's row tiles, and this CTA's half of the contraction
+  const int t_lo = static_cast<int>(static_cast<int64_t>(pair) * p.tiles / p.pairs);
+  const int t_hi = static_cast<int>(static_cast<int64_t>(pair + 1) * p.tiles / p.pairs);
+  const int half = (p.nkb + 1) / 2;
+  const int kb_lo = rank ? half : 0, nb = rank ? p.nkb - half : half;
+
+  for (int t0 = t_lo; t0 < t_hi; t0 += PT) {
+    // the pass's blocks, tile by tile, in one run cut evenly over the warps
+    const int nt = min(PT, t_hi - t0);
+    const int total = nt * nb, chunk = max(1, (total + kClWarps - 1) / kClWarps);
+    const int b0 = min(total, warp * chunk), n = min(total, b0 + chunk) - b0;
+    if (n > 0) {
+      // load cursor: the block to fetch next
+      int lt = b0 / nb, lk = b0 - lt * nb;
+      const uint8_t *c0, *c1;
+      const float *a0, *a1;
+      auto aim = [&]() {
+        const int64_t r0 = min((t0 + lt) * 16 + g, p.N - 1), r1 = min((t0 + lt) * 16 + g + 8, p.N - 1);
+        c0 = p.codes + r0 * row_bytes + 32 * (kb_lo + lk) + 8 * j;
+        c1 = p.codes + r1 * row_bytes + 32 * (kb_lo + lk) + 8 * j;
+        a0 = p.absmax + r0 * p.nkb + kb_lo + lk;
+        a1 = p.absmax + r1 * p.nkb + kb_lo + lk;
+      };
+      aim();
+      uint2 w0[D], w1[D];
+      float s0[D], s1[D];
+      auto fetch = [&](uint2& x0, uint2& x1, float& y0, float& y1) {
+        x0 = cl_ld_codes(c0);
+        x1 = cl_ld_codes(c1);
+        y0 = cl_ld_scale(a0);
+        y1 = cl_ld_scale(a1);
+        if (++lk == nb) {
+          lk = 0;
+          ++lt;
+          aim();
+        } else {
+          c0 += 32; c1 += 32; ++a0; ++a1;
         }
-        float d[4] = {};
+      };
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
-          dc_mma(d[0], d[1], d[2], d[3], a[4 * s], a[4 * s + 1], a[4 * s + 2], a[4 * s + 3], dc_word(x[s >> 1], 2 * (s & 1)),
-                 dc_word(x[s >> 1], 2 * (s & 1) + 1));
-        acc[n][0] = fmaf(s0, d[0], acc[n][0]);
-        acc[n][1] = fmaf(s0, d[1], acc[n][1]);
-        acc[n][2] = fmaf(s1, d[2], acc[n][2]);
-        acc[n][3] = fmaf(s1, d[3], acc[n][3]);
+      for (int s = 0; s < D; ++s)
+        if (s < n) fetch(w0[s], w1[s], s0[s], s1[s]);
+
+      int ck = b0 - (b0 / nb) * nb, seg = 0;
+      float acc[NT][4] = {};
+      auto flush = [&]() {             // this warp's sums of a row tile
+        const uint32_t red = redu + static_cast<uint32_t>((warp * SEG + seg) * 16 * TT * 4);
+#pragma unroll
+        for (int m = 0; m < NT; ++m) {
+          cl_sts2(red + 4u * (g * TT + 8 * m + 2 * j), acc[m][0], acc[m][1]);
+          cl_sts2(red + 4u * ((g + 8) * TT + 8 * m + 2 * j), acc[m][2], acc[m][3]);
+          acc[m][0] = acc[m][1] = acc[m][2] = acc[m][3] = 0.0f;
+        }
+        ++seg;
+      };
+      for (int i = 0; i < n; i += D) {
+#pragma unroll
+        for (int s = 0; s < D; ++s) {
+          if (i + s < n) {
+            const __nv_bfloat16* xk = X + static_cast<int64_t>(64) * (kb_lo + ck) + 16 * j;
+            uint4 x[NT][2];
+#pragma unroll
+            for (int m = 0; m < NT; ++m) {
+              x[m][0] = x[m][1] = make_uint4(0, 0, 0, 0);
+              if (8 * m + g < T) {
+                const uint4* xp = reinterpret_cast<const uint4*>(xk + static_cast<int64_t>(8 * m + g) * K);
+                x[m][0] = __ldg(xp);
+                x[m][1] = __ldg(xp + 1);
+              }
+            }
+            uint32_t a[16];
+            a[0] = dc_pair<0>(w0[s].x, lanebyte);  a[1] = dc_pair<0>(w1[s].x, lanebyte);
+            a[2] = dc_pair<1>(w0[s].x, lanebyte);  a[3] = dc_pair<1>(w1[s].x, lanebyte);
+            a[4] = dc_pair<2>(w0[s].x, lanebyte);  a[5] = dc_pair<2>(w1[s].x, lanebyte);
+            a[6] = dc_pair<3>(w0[s].x, lanebyte);  a[7] = dc_pair<3>(w1[s].x, lanebyte);
+            a[8] = dc_pair<0>(w0[s].y, lanebyte);  a[9] = dc_pair<0>(w1[s].y, lanebyte);
+            a[10] = dc_pair<1>(w0[s].y, lanebyte); a[11] = dc_pair<1>(w1[s].y, lanebyte);
+            a[12] = dc_pair<2>(w0[s].y, lanebyte); a[13] = dc_pair<2>(w1[s].y, lanebyte);
+            a[14] = dc_pair<3>(w0[s].y, lanebyte); a[15] = dc_pair<3>(w1[s].y, lanebyte);
+            const float f0 = s0[s], f1 = s1[s];
+            if (i + s + D < n) fetch(w0[s], w1[s], s0[s], s1[s]);
+#pragma unroll
+            for (int m = 0; m < NT; ++m) {
+              float d[4] = {};
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                dc_mma(d[0], d[1], d[2], d[3], a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3],
+                       dc_word(x[m][q >> 1], 2 * (q & 1)), dc_word(x[m][q >> 1], 2 * (q & 1) + 1));
+              acc[m][0] = fmaf(f0, d[0], acc[m][0]);
+              acc[m][1] = fmaf(f0, d[1], acc[m][1]);
+              acc[m][2] = fmaf(f1, d[2], acc[m][2]);
+              acc[m][3] = fmaf(f1, d[3], acc[m][3]);
+            }
+            if (++ck == nb) {
+              ck = 0;
+              flush();
+            }
+          }
+        }
+      }
+      if (ck != 0) flush();
+    }
+    __syncthreads();
+    // a tile's sums: the warps that cover it, in order, then the pair's second half
+    auto mine = [&](int tile, int e) {
+      float sum = 0.0f;
+      if (nb > 0) {
+        const int first = tile * nb / chunk, last = ((tile + 1) * nb - 1) / chunk;
+        for (int w = first; w <= last; ++w) {
+          const int sg = tile - (w * chunk) / nb;
+          sum += cl_lds(redu + 4u * static_cast<uint32_t>((w * SEG + sg) * 16 * TT + e));
+        }
+      }
+      return sum;
+    };
+    if (rank == 1)
+      for (int i = threadIdx.x; i < nt * 16 * TT; i += blockDim.x)
+        cl_st_peer(base + 4u * i, 0, mine(i / (16 * TT), i % (16 * TT)));
+    cl_cluster_sync();
+    if (rank == 0) {
+      for (int i = threadIdx.x; i < nt * 16 * TT; i += blockDim.x) {
+        const float sum = mine(i / (16 * TT), i % (16 * TT)) + cl_lds(base + 4u * i);
+        const int row = (t0 + i / (16 * TT)) * 16 + (i % (16 * TT)) / TT, t = i % TT;
+        if (row < p.N && t < T) p.Y[static_cast<int64_t>(tok0 + t) * p.N + row] = __float2bfloat16_rn(sum);
       }
     }
-    float* mine = red + warp * 16 * 8 * NT;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      mine[g * 8 * NT + 8 * n + 2 * j] = acc[n][0];
-      mine[g * 8 * NT + 8 * n + 2 * j + 1] = acc[n][1];
-      mine[(g + 8) * 8 * NT + 8 * n + 2 * j] = acc[n][2];
-      mine[(g + 8) * 8 * NT + 8 * n + 2 * j + 1] = acc[n][3];
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < 16 * 8 * NT; i += blockDim.x) {
-      float sum = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kClWarps; ++w) sum += red[w * 16 * 8 * NT + i];
-      const int n = tile * 16 + i / (8 * NT), t = i % (8 * NT);
-      if (n < p.N && t < p.T) p.Y[static_cast<int64_t>(t) * p.N + n] = __float2bfloat16_rn(sum);
-    }
-    __syncthreads();
+    if (t0 + PT < t_hi) cl_cluster_sync();     // both have read their sums before the next pass writes them
   }
 }
 
