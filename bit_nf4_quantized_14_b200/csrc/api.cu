@@ -839,6 +839,20 @@ int launch_codebook_linear(ClParams p, const CodebookArg& cb, int sms, cudaStrea
   return launched();
 }
 
+int launch_codebook_linear1(ClParams p, const CodebookArg& cb, int sms, cudaStream_t st) {
+  const bool vec = p.nkb % 4 == 0;
+  auto kern = vec ? codebook_linear1_kernel<true> : codebook_linear1_kernel<false>;
+  CUtensorMap tc, ts = {};
+  if (!make_tmap_t(&tc, p.codes, TmType::kU8, p.nkb * int64_t(32), p.N, p.nkb * int64_t(32), 256, 8, false) ||
+      (vec && !make_tmap_t(&ts, p.absmax, TmType::kF32, p.nkb, p.N, p.nkb, 8, 8, false)))
+    return cuda_fail(cudaGetLastError(), "tensor-map encode", __LINE__);
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kC1Smem) != cudaSuccess)
+    return cuda_fail(cudaGetLastError(), "cudaFuncSetAttribute", __LINE__);
+  p.tiles = static_cast<int>(cdiv(p.N, 8));
+  kern<<<std::min(p.tiles, sms), kClWarps * 32, kC1Smem, st>>>(tc, ts, p, cb);
+  return launched();
+}
+
 // ---- rotary positions ------------------------------------------------------------------------------
 constexpr double kTwoPi = 6.283185307179586476925286766559;
 
@@ -1378,6 +1392,8 @@ int qlora_codebook_linear(const void* X, int64_t T, const void* codes, const flo
   p.codes = static_cast<const uint8_t*>(codes);
   p.absmax = absmax;
   p.Y = static_cast<__nv_bfloat16*>(Y);
+  // one or two tokens whose X fits in shared memory (K up to 24,500, or 12,200 for two)
+  if (T <= kC1Tokens && c1_x_bytes(T, K / 64) <= kC1XBytes) return launch_codebook_linear1(p, cb, sms, st);
   if (T <= 8) return launch_codebook_linear<1>(p, cb, sms, st);
   if (T <= 16) return launch_codebook_linear<2>(p, cb, sms, st);
   return launch_codebook_linear<4>(p, cb, sms, st);   // above 32: two groups of tokens, the second's weights from L2

@@ -232,4 +232,214 @@ __global__ void __launch_bounds__(kClWarps * 32, 1) __cluster_dims__(2, 1, 1)
   }
 }
 
+// ---- one or two tokens ---------------------------------------------------------------------------------
+// Lookups, X and the codes all pass through the SM's one shared-memory pipe, and with one token that pipe binds
+// as soon as HBM does; so the stream takes as little of it, and as few instructions, as it can. TMA brings units of
+// 8 rows x 256 bytes of codes (two windows of 256 elements, 4 blocks) and their 64 constants into two slots that
+// every warp keeps for itself (no barrier with another warp; 64 KB per SM in flight), refilled as soon as the
+// warp has read them into registers. A warp reads a window with two conflict-free 16-byte loads: lane l has chunk
+// l % 8 of row l / 8 and of that row + 4. In the MMA each quad of
+// lanes is then half a row (chunks 0..3 or 4..7: 128 elements), so the 16 rows of the A operand are 8 weight rows x
+// 2 halves h, and the 8 columns of B keep the halves and the two blocks e inside each apart: column 4 t + 2 h + e
+// is x of token t and half h, zero except where lane j holds block e = j / 2 (those lanes' registers stay zero:
+// they take no part in the load). Lane (g, j) with g = 2 r + h finds the sums of blocks 2 h and 2 h + 1 of row r
+// (and r + 4) and token t in its own accumulators where j = 2 t + h. A CTA owns a run of 8-row tiles, cut evenly
+// over its warps. (Loads into registers 4 windows ahead took 39 us for 22016 x 8192: the lookups' waits shared
+// scoreboards with the loads in flight.)
+constexpr int kC1Ring = 2;
+constexpr int kC1Pass = 64;               // tiles per pass
+constexpr int kC1Seg = kC1Pass / kClWarps + 2;
+constexpr int kC1Tokens = 2;
+constexpr int kC1CodeBytes = 8 * 256, kC1ScaleBytes = 8 * 8 * 4, kC1SlotBytes = kC1CodeBytes + kC1ScaleBytes;
+constexpr uint32_t kC1Slots = 2u << 16;   // above the table: the warps' slots, then their barriers
+constexpr uint32_t kC1Bars = kC1Slots + kClWarps * kC1Ring * kC1SlotBytes;
+constexpr int kC1Smem = static_cast<int>(kC1Bars) + kClWarps * kC1Ring * 8;
+constexpr int kC1RedBytes = kClWarps * kC1Seg * 32 * 4;       // below it: the warps' sums, then X
+constexpr int kC1XBytes = 65536 - kClBaseMax - kC1RedBytes;
+static_assert(kC1Smem <= 227 * 1024 && kC1SlotBytes % 128 == 0 && kC1RedBytes % 128 == 0, "shared memory");
+static_assert(kC1Ring == 2, "the slot and its phase are tracked as one toggle each");
+__host__ __device__ constexpr int64_t c1_x_bytes(int64_t T, int64_t nkb) { return T * ((nkb + 7) / 8 * 1024); }
+
+__device__ __forceinline__ void c1_tma(uint32_t dst, const void* map, uint32_t bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(map), "r"(bar), "r"(c0), "r"(c1)
+      : "memory");
+}
+__device__ __forceinline__ void c1_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+// One fp32 (or a zero) global -> shared, and this thread's arrival on `bar` once its copies so far are complete.
+__device__ __forceinline__ void c1_cp4(uint32_t dst, const void* src, uint32_t src_bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+__device__ __forceinline__ void c1_cp_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void c1_ldx(uint4& x, uint32_t addr, uint32_t on) {   // lanes without x keep their zeros
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t@p ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "+r"(x.x), "+r"(x.y), "+r"(x.z), "+r"(x.w)
+      : "r"(addr), "r"(on));
+}
+__device__ __forceinline__ void c1_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// VEC: rows of constants are 16-byte aligned (K % 256 == 0) and come by TMA too; otherwise by 4-byte copies.
+template <bool VEC>
+__global__ void __launch_bounds__(kClWarps * 32, 1)
+    codebook_linear1_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmS,
+                            const __grid_constant__ ClParams p, const __grid_constant__ CodebookArg cb) {
+  extern __shared__ __align__(1024) uint8_t cl_smem[];
+  const uint32_t base = smem_u32(cl_smem), window = base & 0xFF000000u;
+  const uint32_t table = window | kClTable, xs = base + kC1RedBytes;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int g = lane >> 2, j = lane & 3;
+  if (base - window > kClBaseMax) {
+    if (threadIdx.x == 0) raise_status(kStatusTimeout);
+    return;
+  }
+  const uint32_t slots = (window | kC1Slots) + warp * kC1Ring * kC1SlotBytes;
+  const uint32_t bars = (window | kC1Bars) + warp * kC1Ring * 8;
+  if (lane == 0) {
+    for (int s = 0; s < kC1Ring; ++s)
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bars + 8 * s), "r"(VEC ? 1 : 33));
+    fence_barrier_init();
+  }
+  const int nu = (p.nkb + 7) / 8;                // units per row
+  for (int i = threadIdx.x; i < 256 * 32; i += blockDim.x) {
+    const uint32_t v = pack_bf16x2(cb.levels[i >> 9], cb.levels[(i >> 5) & 15]);
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(table + (static_cast<uint32_t>(i >> 5) << 8) + 4u * (i & 31)), "r"(v)
+                 : "memory");
+  }
+  // X window by window, padded with zeros: 16-byte piece q of (half h, lane j) at 128 q + 16 (4 h + j)
+  for (int i = threadIdx.x; i < p.T * nu * 64; i += blockDim.x) {
+    const int t = i / (nu * 64), c = i - t * nu * 64;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (c < p.nkb * 8) v = __ldg(reinterpret_cast<const uint4*>(p.X + static_cast<int64_t>(t) * p.nkb * 64) + c);
+    st_shared_v4(xs + 512u * (t * nu * 2 + (c >> 5)) + 128u * (c & 3) + 16u * ((c >> 2) & 7), v.x, v.y, v.z, v.w);
+  }
+  __syncthreads();
+  const uint32_t lanebyte = table | (4u * lane);
+
+  // B operand: column g = 4 t + 2 h + e; this lane's 32 elements of half h, if they are of block e
+  const int bt = g >> 2;
+  const uint32_t on = (bt < p.T && (j >> 1) == (g & 1)) ? 1u : 0u;
+  const uint32_t x_base = xs + 1024u * (bt * nu) + 16u * (4 * ((g >> 1) & 1) + j);
+  // A operand: 16 bytes of row l / 8 (and that + 4); its blocks of a window begin at 2 h
+  const int ar = lane >> 3, h = (lane >> 2) & 1;
+  const uint32_t code_off = 256u * ar + 16u * (lane & 7), scale_off = kC1CodeBytes + 32u * ar + 8u * h;
+  uint4 x[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) x[q] = make_uint4(0, 0, 0, 0);
+
+  const int t_lo = static_cast<int>(static_cast<int64_t>(blockIdx.x) * p.tiles / gridDim.x);
+  const int t_hi = static_cast<int>(static_cast<int64_t>(blockIdx.x + 1) * p.tiles / gridDim.x);
+  uint32_t in_slot = 0, slot = 0, phase = 0;     // the slots to fill and to read next
+  bool ok = true;
+  for (int t0 = t_lo; t0 < t_hi; t0 += kC1Pass) {
+    const int nt = min(kC1Pass, t_hi - t0);
+    const int total = nt * nu, chunk = (total + kClWarps - 1) / kClWarps;
+    const int b0 = min(total, warp * chunk), n = min(total, b0 + chunk) - b0;
+    int issued = 0, i = 0;
+    if (n > 0) {
+      int ck = b0 % nu, seg = 0;                 // the unit to read next
+      int lk = ck, row = (t0 + b0 / nu) * 8;     // the unit to fetch next
+      auto fetch = [&]() {
+        const uint32_t dst = slots + in_slot * kC1SlotBytes, bar = bars + 8 * in_slot;
+        if constexpr (!VEC) {
+#pragma unroll
+          for (int e = lane; e < 64; e += 32) {
+            const int r = row + (e >> 3), kb = lk * 8 + (e & 7);
+            const bool in = r < p.N && kb < p.nkb;
+            c1_cp4(dst + kC1CodeBytes + 4u * e, p.absmax + (in ? static_cast<int64_t>(r) * p.nkb + kb : 0), in ? 4u : 0u);
+          }
+          c1_cp_arrive(bar);
+        }
+        if (lane == 0) {
+          c1_expect(bar, VEC ? kC1SlotBytes : kC1CodeBytes);
+          c1_tma(dst, &tmC, bar, lk * 256, row);
+          if constexpr (VEC) c1_tma(dst + kC1CodeBytes, &tmS, bar, lk * 8, row);
+        }
+        in_slot ^= 1;
+        ++issued;
+        if (++lk == nu) { lk = 0; row += 8; }
+      };
+      fetch();
+      if (n > 1) fetch();
+      uint32_t xa = x_base + 1024u * ck;
+      float acc0 = 0.0f, acc1 = 0.0f;
+      auto flush = [&]() {      // rows r and r + 4 of token t = j / 2, half h = j % 2 (where that is this lane's)
+        if ((j & 1) == h) {
+          const uint32_t red = base + static_cast<uint32_t>((warp * kC1Seg + seg) * 128) + 4u * (j >> 1);
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(red + 8u * (2 * ar + h)), "f"(acc0) : "memory");
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(red + 8u * (2 * (ar + 4) + h)), "f"(acc1) : "memory");
+        }
+        acc0 = acc1 = 0.0f;
+        ++seg;
+      };
+      for (; i < n; ++i) {
+        if (!__all_sync(0xffffffffu, ok && mbar_wait_addr(bars + 8 * slot, phase))) { ok = false; break; }
+        const uint32_t at = slots + slot * kC1SlotBytes;
+        uint4 w[4];
+        float2 sc[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {            // window u / 2, rows + 4 (u % 2)
+          w[u] = dc_ld128(at + code_off + 1024u * (u & 1) + 128u * (u >> 1));
+          sc[u] = dc_ldf2(at + scale_off + 128u * (u & 1) + 16u * (u >> 1));
+        }
+        __syncwarp();           // the slot has been read
+        slot ^= 1;
+        phase ^= slot ^ 1;
+        if (issued < n) fetch();
+#pragma unroll
+        for (int u = 0; u < 4; u += 2) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) c1_ldx(x[q], xa + 256u * u + 128u * q, on);
+          float d0[4] = {}, d1[4] = {};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {          // 8 elements of the lane's 32 at a time: one word of codes
+            const uint32_t u0 = dc_word(w[u], q), u1 = dc_word(w[u + 1], q);
+            c1_mma(d0, dc_pair<0>(u0, lanebyte), dc_pair<0>(u1, lanebyte), dc_pair<1>(u0, lanebyte), dc_pair<1>(u1, lanebyte),
+                   x[q].x, x[q].y);
+            c1_mma(d1, dc_pair<2>(u0, lanebyte), dc_pair<2>(u1, lanebyte), dc_pair<3>(u0, lanebyte), dc_pair<3>(u1, lanebyte),
+                   x[q].z, x[q].w);
+          }
+          acc0 = fmaf(sc[u].x, d0[0] + d1[0], fmaf(sc[u].y, d0[1] + d1[1], acc0));
+          acc1 = fmaf(sc[u + 1].x, d0[2] + d1[2], fmaf(sc[u + 1].y, d0[3] + d1[3], acc1));
+        }
+        xa += 1024;
+        if (++ck == nu) {
+          ck = 0;
+          xa = x_base;
+          flush();
+        }
+      }
+      if (ok && ck != 0) flush();
+      for (; i < issued; ++i) {      // after a wait that gave up: wait shortly for this warp's copies in flight
+        mbar_wait_short_addr(bars + 8 * slot, phase);
+        slot ^= 1;
+        phase ^= slot ^ 1;
+      }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < nt * 8 * p.T; e += blockDim.x) {
+      const int tile = e / (8 * p.T), r = e / p.T % 8, t = e % p.T;
+      const int first = tile * nu / chunk, last = ((tile + 1) * nu - 1) / chunk;
+      float sum = 0.0f;
+      for (int v = first; v <= last; ++v) {
+        const uint32_t red = base + static_cast<uint32_t>((v * kC1Seg + tile - (v * chunk) / nu) * 128) + 16u * r + 4u * t;
+        sum += cl_lds(red) + cl_lds(red + 8u);
+      }
+      const int out = (t0 + tile) * 8 + r;
+      if (out < p.N) p.Y[static_cast<int64_t>(t) * p.N + out] = __float2bfloat16_rn(sum);
+    }
+    __syncthreads();
+  }
+}
+
 }  // namespace qnf4

@@ -52,44 +52,48 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t by
                "r"(bytes)
                : "memory");
 }
-__device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_try_wait_addr(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
+      : "r"(bar), "r"(parity)
       : "memory");
   return ok != 0;
 }
 // The same test, but a thread whose phase is not complete may be suspended (up to hint_ns) until it
 // completes: a waiting warp then takes no issue slots from the warps that compute beside it.
-__device__ __forceinline__ bool mbar_try_wait_suspend(uint64_t* bar, uint32_t parity, uint32_t hint_ns) {
+__device__ __forceinline__ bool mbar_try_wait_suspend_addr(uint32_t bar, uint32_t parity, uint32_t hint_ns) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(hint_ns)
+      : "r"(bar), "r"(parity), "r"(hint_ns)
       : "memory");
   return ok != 0;
+}
+__device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
+  return mbar_try_wait_addr(smem_u32(bar), parity);
 }
 // Wait for the phase with the given parity to complete. Returns false (and records a timeout in the
 // status word) if it has not completed within the wait limit in force (g_wait_limit_ns).
 constexpr uint32_t kSuspendHintNs = 20000;
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return true;
+__device__ __forceinline__ bool mbar_wait_addr(uint32_t bar, uint32_t parity) {   // bar: a shared address
+  if (mbar_try_wait_addr(bar, parity)) return true;
   const unsigned long long t0 = globaltimer_ns(), limit = *(volatile unsigned long long*)&g_wait_limit_ns;
   while (true) {
-    if (mbar_try_wait_suspend(bar, parity, kSuspendHintNs)) return true;
+    if (mbar_try_wait_suspend_addr(bar, parity, kSuspendHintNs)) return true;
     if (globaltimer_ns() - t0 > limit) {
       raise_status(kStatusTimeout);
       return false;
     }
   }
 }
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) { return mbar_wait_addr(smem_u32(bar), parity); }
 // Wait until the 64-bit word at p (global memory, written by another CTA of the same grid) equals
 // `want`, with acquire ordering for what its writer published before it. Bounded like mbar_wait.
 __device__ __forceinline__ uint64_t ld_acquire_u64(const uint64_t* p) {
@@ -113,12 +117,15 @@ __device__ __forceinline__ bool wait_word_eq(const uint64_t* p, uint64_t want) {
   }
 }
 // Same, with a short limit, for draining in-flight copies after another role gave up.
-__device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_wait_short_addr(uint32_t bar, uint32_t parity) {
   const unsigned long long t0 = globaltimer_ns();
-  while (!mbar_try_wait(bar, parity)) {
+  while (!mbar_try_wait_addr(bar, parity)) {
     if (globaltimer_ns() - t0 > 100000000ull) return false;
   }
   return true;
+}
+__device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity) {
+  return mbar_wait_short_addr(smem_u32(bar), parity);
 }
 
 // ------------------------------------------------------------------------------------------------
