@@ -166,11 +166,12 @@ bool make_codebook(const float* lv, int nl, CodebookArg* cb, BucketArg* bk) {
 // Launch with programmatic stream serialization: the kernel may start while its predecessor in the
 // stream drains, and waits for it (griddepcontrol.wait) before touching its results.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kern)(KArgs...), unsigned grid, unsigned block, cudaStream_t st, Args... args) {
+cudaError_t launch_pdl_smem(void (*kern)(KArgs...), dim3 grid, unsigned block, size_t smem, cudaStream_t st,
+                            Args... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = 0;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -178,6 +179,10 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), unsigned grid, unsigned block, cu
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+}
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl(void (*kern)(KArgs...), unsigned grid, unsigned block, cudaStream_t st, Args... args) {
+  return launch_pdl_smem(kern, dim3(grid), block, 0, st, args...);
 }
 
 // Workspace of the quantizer: per-block constants (fp32), per-slab tree sums (fp64), the mean pass's
@@ -849,7 +854,8 @@ int launch_codebook_linear1(ClParams p, const CodebookArg& cb, int sms, cudaStre
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kC1Smem) != cudaSuccess)
     return cuda_fail(cudaGetLastError(), "cudaFuncSetAttribute", __LINE__);
   p.tiles = static_cast<int>(cdiv(p.N, 8));
-  kern<<<std::min(p.tiles, sms), kClWarps * 32, kC1Smem, st>>>(tc, ts, p, cb);
+  if (launch_pdl_smem(kern, dim3(std::min(p.tiles, sms)), kClWarps * 32, kC1Smem, st, tc, ts, p, cb) != cudaSuccess)
+    return cuda_fail(cudaGetLastError(), "cudaLaunchKernelEx", __LINE__);
   return launched();
 }
 

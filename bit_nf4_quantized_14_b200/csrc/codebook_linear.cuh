@@ -316,14 +316,11 @@ __global__ void __launch_bounds__(kClWarps * 32, 1)
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(table + (static_cast<uint32_t>(i >> 5) << 8) + 4u * (i & 31)), "r"(v)
                  : "memory");
   }
-  // X window by window, padded with zeros: 16-byte piece q of (half h, lane j) at 128 q + 16 (4 h + j)
-  for (int i = threadIdx.x; i < p.T * nu * 64; i += blockDim.x) {
-    const int t = i / (nu * 64), c = i - t * nu * 64;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (c < p.nkb * 8) v = __ldg(reinterpret_cast<const uint4*>(p.X + static_cast<int64_t>(t) * p.nkb * 64) + c);
-    st_shared_v4(xs + 512u * (t * nu * 2 + (c >> 5)) + 128u * (c & 3) + 16u * ((c >> 2) & 7), v.x, v.y, v.z, v.w);
-  }
-  __syncthreads();
+  // All of the above reads nothing of the kernel before this one in the stream and may run beside its end; the
+  // next kernel may do the same beside this one's.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __syncwarp();
   const uint32_t lanebyte = table | (4u * lane);
 
   // B operand: column g = 4 t + 2 h + e; this lane's 32 elements of half h, if they are of block e
@@ -340,12 +337,23 @@ __global__ void __launch_bounds__(kClWarps * 32, 1)
   const int t_lo = static_cast<int>(static_cast<int64_t>(blockIdx.x) * p.tiles / gridDim.x);
   const int t_hi = static_cast<int>(static_cast<int64_t>(blockIdx.x + 1) * p.tiles / gridDim.x);
   uint32_t in_slot = 0, slot = 0, phase = 0;     // the slots to fill and to read next
+  auto stage_x = [&]() {
+    // X window by window, padded with zeros: 16-byte piece q of (half h, lane j) at 128 q + 16 (4 h + j)
+    for (int i = threadIdx.x; i < p.T * nu * 64; i += blockDim.x) {
+      const int t = i / (nu * 64), c = i - t * nu * 64;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (c < p.nkb * 8) v = __ldg(reinterpret_cast<const uint4*>(p.X + static_cast<int64_t>(t) * p.nkb * 64) + c);
+      st_shared_v4(xs + 512u * (t * nu * 2 + (c >> 5)) + 128u * (c & 3) + 16u * ((c >> 2) & 7), v.x, v.y, v.z, v.w);
+    }
+    __syncthreads();
+  };
   bool ok = true;
   for (int t0 = t_lo; t0 < t_hi; t0 += kC1Pass) {
     const int nt = min(kC1Pass, t_hi - t0);
     const int total = nt * nu, chunk = (total + kClWarps - 1) / kClWarps;
     const int b0 = min(total, warp * chunk), n = min(total, b0 + chunk) - b0;
     int issued = 0, i = 0;
+    if (n == 0 && t0 == t_lo) stage_x();
     if (n > 0) {
       int ck = b0 % nu, seg = 0;                 // the unit to read next
       int lk = ck, row = (t0 + b0 / nu) * 8;     // the unit to fetch next
@@ -371,6 +379,7 @@ __global__ void __launch_bounds__(kClWarps * 32, 1)
       };
       fetch();
       if (n > 1) fetch();
+      if (t0 == t_lo) stage_x();      // while the first units are on their way
       uint32_t xa = x_base + 1024u * ck;
       float acc0 = 0.0f, acc1 = 0.0f;
       auto flush = [&]() {      // rows r and r + 4 of token t = j / 2, half h = j % 2 (where that is this lane's)
