@@ -854,8 +854,21 @@ int launch_codebook_linear1(ClParams p, const CodebookArg& cb, int sms, cudaStre
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kC1Smem) != cudaSuccess)
     return cuda_fail(cudaGetLastError(), "cudaFuncSetAttribute", __LINE__);
   p.tiles = static_cast<int>(cdiv(p.N, 8));
-  if (launch_pdl_smem(kern, dim3(std::min(p.tiles, sms)), kClWarps * 32, kC1Smem, st, tc, ts, p, cb) != cudaSuccess)
+  if (launch_pdl_smem(kern, dim3(std::min(p.tiles, sms)), kC1Warps * 32, kC1Smem, st, tc, ts, p, cb) != cudaSuccess)
     return cuda_fail(cudaGetLastError(), "cudaLaunchKernelEx", __LINE__);
+  return launched();
+}
+
+template <int NT>
+int launch_codebook_linear4(ClParams p, const CodebookArg& cb, int sms, cudaStream_t st) {
+  auto kern = codebook_linear4_kernel<NT>;
+  CUtensorMap tc;
+  if (!make_tmap_t(&tc, p.codes, TmType::kU8, p.nkb * int64_t(32), p.N, p.nkb * int64_t(32), 128, 16, true))
+    return cuda_fail(cudaGetLastError(), "tensor-map encode", __LINE__);
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kC4Smem) != cudaSuccess)
+    return cuda_fail(cudaGetLastError(), "cudaFuncSetAttribute", __LINE__);
+  p.pairs = std::max(1, std::min(p.tiles, sms / 2));
+  kern<<<2 * p.pairs, kC4Warps * 32, kC4Smem, st>>>(tc, p, cb);
   return launched();
 }
 
@@ -1400,8 +1413,8 @@ int qlora_codebook_linear(const void* X, int64_t T, const void* codes, const flo
   p.Y = static_cast<__nv_bfloat16*>(Y);
   // one or two tokens whose X fits in shared memory (K up to 24,500, or 12,200 for two)
   if (T <= kC1Tokens && c1_x_bytes(T, K / 64) <= kC1XBytes) return launch_codebook_linear1(p, cb, sms, st);
-  if (T <= 8) return launch_codebook_linear<1>(p, cb, sms, st);
-  if (T <= 16) return launch_codebook_linear<2>(p, cb, sms, st);
+  if (T <= 8) return launch_codebook_linear4<1>(p, cb, sms, st);
+  if (T <= 16) return launch_codebook_linear4<2>(p, cb, sms, st);
   return launch_codebook_linear<4>(p, cb, sms, st);   // above 32: two groups of tokens, the second's weights from L2
 }
 

@@ -246,15 +246,16 @@ __global__ void __launch_bounds__(kClWarps * 32, 1) __cluster_dims__(2, 1, 1)
 // (and r + 4) and token t in its own accumulators where j = 2 t + h. A CTA owns a run of 8-row tiles, cut evenly
 // over its warps. (Loads into registers 4 windows ahead took 39 us for 22016 x 8192: the lookups' waits shared
 // scoreboards with the loads in flight.)
+constexpr int kC1Warps = 16;              // 12 to 20 measure alike: the shared-memory pipe binds, not latency
 constexpr int kC1Ring = 2;
 constexpr int kC1Pass = 64;               // tiles per pass
-constexpr int kC1Seg = kC1Pass / kClWarps + 2;
+constexpr int kC1Seg = kC1Pass / kC1Warps + 2;
 constexpr int kC1Tokens = 2;
 constexpr int kC1CodeBytes = 8 * 256, kC1ScaleBytes = 8 * 8 * 4, kC1SlotBytes = kC1CodeBytes + kC1ScaleBytes;
 constexpr uint32_t kC1Slots = 2u << 16;   // above the table: the warps' slots, then their barriers
-constexpr uint32_t kC1Bars = kC1Slots + kClWarps * kC1Ring * kC1SlotBytes;
-constexpr int kC1Smem = static_cast<int>(kC1Bars) + kClWarps * kC1Ring * 8;
-constexpr int kC1RedBytes = kClWarps * kC1Seg * 32 * 4;       // below it: the warps' sums, then X
+constexpr uint32_t kC1Bars = kC1Slots + kC1Warps * kC1Ring * kC1SlotBytes;
+constexpr int kC1Smem = static_cast<int>(kC1Bars) + kC1Warps * kC1Ring * 8;
+constexpr int kC1RedBytes = kC1Warps * kC1Seg * 32 * 4;       // below it: the warps' sums, then X
 constexpr int kC1XBytes = 65536 - kClBaseMax - kC1RedBytes;
 static_assert(kC1Smem <= 227 * 1024 && kC1SlotBytes % 128 == 0 && kC1RedBytes % 128 == 0, "shared memory");
 static_assert(kC1Ring == 2, "the slot and its phase are tracked as one toggle each");
@@ -291,7 +292,7 @@ __device__ __forceinline__ void c1_mma(float (&d)[4], uint32_t a0, uint32_t a1, 
 
 // VEC: rows of constants are 16-byte aligned (K % 256 == 0) and come by TMA too; otherwise by 4-byte copies.
 template <bool VEC>
-__global__ void __launch_bounds__(kClWarps * 32, 1)
+__global__ void __launch_bounds__(kC1Warps * 32, 1)
     codebook_linear1_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmS,
                             const __grid_constant__ ClParams p, const __grid_constant__ CodebookArg cb) {
   extern __shared__ __align__(1024) uint8_t cl_smem[];
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(kClWarps * 32, 1)
   bool ok = true;
   for (int t0 = t_lo; t0 < t_hi; t0 += kC1Pass) {
     const int nt = min(kC1Pass, t_hi - t0);
-    const int total = nt * nu, chunk = (total + kClWarps - 1) / kClWarps;
+    const int total = nt * nu, chunk = (total + kC1Warps - 1) / kC1Warps;
     const int b0 = min(total, warp * chunk), n = min(total, b0 + chunk) - b0;
     int issued = 0, i = 0;
     if (n == 0 && t0 == t_lo) stage_x();
@@ -448,6 +449,181 @@ __global__ void __launch_bounds__(kClWarps * 32, 1)
       if (out < p.N) p.Y[static_cast<int64_t>(t) * p.N + out] = __float2bfloat16_rn(sum);
     }
     __syncthreads();
+  }
+}
+
+// ---- 3 to 16 tokens -------------------------------------------------------------------------------------
+// X no longer fits beside the stream, and reading its fragments once per 16 rows would cost the shared-memory
+// pipe more than the lookups do. So a warp keeps the fragments of 256 elements of all tokens in registers (64 of
+// them for 16 tokens) and runs up to 4 tiles of 16 rows past them, with their accumulators in registers too. A
+// CTA pair owns a run of row tiles; its 16 warps each have their own share of the contraction, cut at blocks, and
+// their sums meet at the end of a pass of 4 tiles. Codes come by TMA into 5 slots per warp (16 rows x 128 bytes,
+// 128-byte swizzle; quad g takes row 2 (g % 4) + g / 4 of each 8, whose 8-byte loads then hit distinct banks),
+// constants by 4-byte copies (any alignment).
+constexpr int kC4Warps = 8, kC4Ring = 5, kC4Tiles = 4;
+constexpr int kC4CodeBytes = 16 * 128, kC4ScaleBytes = 16 * 4 * 4;
+constexpr uint32_t kC4Slots = 2u << 16;
+constexpr uint32_t kC4Scales = kC4Slots + kC4Warps * kC4Ring * kC4CodeBytes;
+constexpr uint32_t kC4Bars = kC4Scales + kC4Warps * kC4Ring * kC4ScaleBytes;
+constexpr int kC4Smem = static_cast<int>(kC4Bars) + kC4Warps * kC4Ring * 8;
+__host__ __device__ constexpr int c4_peer_bytes(int NT) { return kC4Tiles * 16 * 8 * NT * 4; }
+static_assert(kC4Smem <= 227 * 1024 && kClBaseMax + (kC4Warps + 1) * c4_peer_bytes(2) <= 65536, "shared memory");
+
+template <int NT>
+__global__ void __launch_bounds__(kC4Warps * 32, 1) __cluster_dims__(2, 1, 1)
+    codebook_linear4_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ ClParams p,
+                            const __grid_constant__ CodebookArg cb) {
+  constexpr int TT = 8 * NT, R = kC4Ring;
+  extern __shared__ __align__(1024) uint8_t cl_smem[];
+  const uint32_t base = smem_u32(cl_smem), window = base & 0xFF000000u;
+  const uint32_t table = window | kClTable;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int g = lane >> 2, j = lane & 3;
+  const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1;
+  if (base - window > kClBaseMax) {
+    if (threadIdx.x == 0) raise_status(kStatusTimeout);
+    return;
+  }
+  const uint32_t slots = (window | kC4Slots) + warp * R * kC4CodeBytes;
+  const uint32_t scales = window + kC4Scales + warp * R * kC4ScaleBytes;
+  const uint32_t bars = window + kC4Bars + warp * R * 8;
+  const uint32_t red = base + c4_peer_bytes(NT);     // the warps' sums; the pair's second half hands over at base
+  if (lane == 0) {
+    for (int s = 0; s < R; ++s) asm volatile("mbarrier.init.shared::cta.b64 [%0], 33;" ::"r"(bars + 8 * s));
+    fence_barrier_init();
+  }
+  for (int i = threadIdx.x; i < 256 * 32; i += blockDim.x) {
+    const uint32_t v = pack_bf16x2(cb.levels[i >> 9], cb.levels[(i >> 5) & 15]);
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(table + (static_cast<uint32_t>(i >> 5) << 8) + 4u * (i & 31)), "r"(v)
+                 : "memory");
+  }
+  cl_cluster_sync();
+  const uint32_t lanebyte = table | (4u * lane);
+  const int gr = 2 * (g & 3) + (g >> 2);             // quad g's row of each 8
+
+  const int t_lo = static_cast<int>(static_cast<int64_t>(pair) * p.tiles / p.pairs);
+  const int t_hi = static_cast<int>(static_cast<int64_t>(pair + 1) * p.tiles / p.pairs);
+  const int part = rank * kC4Warps + warp;           // this warp's share of the blocks
+  const int k_lo = static_cast<int>(static_cast<int64_t>(part) * p.nkb / (2 * kC4Warps));
+  const int k_hi = static_cast<int>(static_cast<int64_t>(part + 1) * p.nkb / (2 * kC4Warps));
+  const int nu = (k_hi - k_lo + 3) / 4;
+  uint32_t in_slot = 0, slot = 0, phase = 0;
+  bool ok = true;
+  for (int t0 = t_lo; t0 < t_hi; t0 += kC4Tiles) {
+    const int nt = min(kC4Tiles, t_hi - t0), n = nu * nt;
+    int issued = 0, done = 0, fk = k_lo, ft = 0;     // the unit to fetch next: block fk, tile ft
+    auto fetch = [&]() {
+      const uint32_t bar = bars + 8 * in_slot, sdst = scales + in_slot * kC4ScaleBytes;
+      const int row = (t0 + ft) * 16;
+#pragma unroll
+      for (int e = lane; e < 64; e += 32) {
+        const int r = row + (e >> 2), kb = fk + (e & 3);
+        const bool in = r < p.N && kb < k_hi;        // blocks of the next warp's share: a constant of 0
+        c1_cp4(sdst + 4u * e, p.absmax + (in ? static_cast<int64_t>(r) * p.nkb + kb : 0), in ? 4u : 0u);
+      }
+      c1_cp_arrive(bar);
+      if (lane == 0) {
+        c1_expect(bar, kC4CodeBytes);
+        c1_tma(slots + in_slot * kC4CodeBytes, &tmC, bar, fk * 32, row);
+      }
+      in_slot = in_slot + 1 == R ? 0 : in_slot + 1;
+      ++issued;
+      if (++ft == nt) { ft = 0; fk += 4; }
+    };
+    for (int s = 0; s < R && s < n; ++s) fetch();
+    float acc[kC4Tiles][NT][4] = {};
+    for (int u = 0; u < nu && ok; ++u) {
+      uint4 x[4][NT][2];
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+#pragma unroll
+        for (int m = 0; m < NT; ++m) {
+          x[b][m][0] = x[b][m][1] = make_uint4(0, 0, 0, 0);
+          const int kb = k_lo + 4 * u + b;
+          if (8 * m + g < p.T && kb < k_hi) {
+            const uint4* xp = reinterpret_cast<const uint4*>(p.X + (static_cast<int64_t>(8 * m + g) * p.nkb + kb) * 64 + 16 * j);
+            x[b][m][0] = __ldg(xp);
+            x[b][m][1] = __ldg(xp + 1);
+          }
+        }
+#pragma unroll
+      for (int t = 0; t < kC4Tiles; ++t) {
+        if (t >= nt || !ok) break;
+        if (!__all_sync(0xffffffffu, mbar_wait_addr(bars + 8 * slot, phase))) { ok = false; break; }
+        const uint32_t at = slots + slot * kC4CodeBytes + 128u * gr + 8u * (j & 1);
+        const uint32_t sa = scales + slot * kC4ScaleBytes + 16u * gr;
+        uint2 w[4][2];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const uint32_t c = at + (static_cast<uint32_t>((2 * b + (j >> 1)) ^ gr) << 4);
+          w[b][0] = dc_ld64(c);
+          w[b][1] = dc_ld64(c + 1024);
+        }
+        const uint4 f0 = dc_ld128(sa), f1 = dc_ld128(sa + 128);
+        __syncwarp();                                // the slot has been read
+        slot = slot + 1 == R ? 0 : slot + 1;
+        phase ^= slot == 0 ? 1u : 0u;
+        ++done;
+        if (issued < n) fetch();
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const uint2 u0 = w[b][0], u1 = w[b][1];
+          uint32_t a[16];
+          a[0] = dc_pair<0>(u0.x, lanebyte);  a[1] = dc_pair<0>(u1.x, lanebyte);
+          a[2] = dc_pair<1>(u0.x, lanebyte);  a[3] = dc_pair<1>(u1.x, lanebyte);
+          a[4] = dc_pair<2>(u0.x, lanebyte);  a[5] = dc_pair<2>(u1.x, lanebyte);
+          a[6] = dc_pair<3>(u0.x, lanebyte);  a[7] = dc_pair<3>(u1.x, lanebyte);
+          a[8] = dc_pair<0>(u0.y, lanebyte);  a[9] = dc_pair<0>(u1.y, lanebyte);
+          a[10] = dc_pair<1>(u0.y, lanebyte); a[11] = dc_pair<1>(u1.y, lanebyte);
+          a[12] = dc_pair<2>(u0.y, lanebyte); a[13] = dc_pair<2>(u1.y, lanebyte);
+          a[14] = dc_pair<3>(u0.y, lanebyte); a[15] = dc_pair<3>(u1.y, lanebyte);
+          const float s0 = __uint_as_float(dc_word(f0, b)), s1 = __uint_as_float(dc_word(f1, b));
+#pragma unroll
+          for (int m = 0; m < NT; ++m) {
+            float d[4] = {};
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              c1_mma(d, a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3], dc_word(x[b][m][q >> 1], 2 * (q & 1)),
+                     dc_word(x[b][m][q >> 1], 2 * (q & 1) + 1));
+            acc[t][m][0] = fmaf(s0, d[0], acc[t][m][0]);
+            acc[t][m][1] = fmaf(s0, d[1], acc[t][m][1]);
+            acc[t][m][2] = fmaf(s1, d[2], acc[t][m][2]);
+            acc[t][m][3] = fmaf(s1, d[3], acc[t][m][3]);
+          }
+        }
+      }
+    }
+    for (; done < issued; ++done) {                  // after a wait that gave up: this warp's copies in flight
+      mbar_wait_short_addr(bars + 8 * slot, phase);
+      slot = slot + 1 == R ? 0 : slot + 1;
+      phase ^= slot == 0 ? 1u : 0u;
+    }
+#pragma unroll
+    for (int t = 0; t < kC4Tiles; ++t)
+#pragma unroll
+      for (int m = 0; m < NT; ++m) {
+        const uint32_t to = red + static_cast<uint32_t>(warp) * c4_peer_bytes(NT) + 4u * ((t * 16 + gr) * TT + 8 * m + 2 * j);
+        cl_sts2(to, acc[t][m][0], acc[t][m][1]);
+        cl_sts2(to + 4u * 8 * TT, acc[t][m][2], acc[t][m][3]);
+      }
+    __syncthreads();
+    auto mine = [&](int e) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kC4Warps; ++w) sum += cl_lds(red + static_cast<uint32_t>(w) * c4_peer_bytes(NT) + 4u * e);
+      return sum;
+    };
+    if (rank == 1)
+      for (int e = threadIdx.x; e < nt * 16 * TT; e += blockDim.x) cl_st_peer(base + 4u * e, 0, mine(e));
+    cl_cluster_sync();
+    if (rank == 0) {
+      for (int e = threadIdx.x; e < nt * 16 * TT; e += blockDim.x) {
+        const float sum = mine(e) + cl_lds(base + 4u * e);
+        const int row = t0 * 16 + e / TT, t = e % TT;
+        if (row < p.N && t < p.T) p.Y[static_cast<int64_t>(t) * p.N + row] = __float2bfloat16_rn(sum);
+      }
+    }
+    if (t0 + kC4Tiles < t_hi) cl_cluster_sync();     // both have read their sums before the next pass writes them
   }
 }
 
