@@ -456,24 +456,26 @@ __global__ void __launch_bounds__(kC1Warps * 32, 1)
 // X no longer fits beside the stream, and reading its fragments once per 16 rows would cost the shared-memory
 // pipe more than the lookups do. So a warp keeps the fragments of 256 elements of all tokens in registers (64 of
 // them for 16 tokens) and runs up to 4 tiles of 16 rows past them, with their accumulators in registers too. A
-// CTA pair owns a run of row tiles; its 16 warps each have their own share of the contraction, cut at blocks, and
-// their sums meet at the end of a pass of 4 tiles. Codes come by TMA into 5 slots per warp (16 rows x 128 bytes,
-// 128-byte swizzle; quad g takes row 2 (g % 4) + g / 4 of each 8, whose 8-byte loads then hit distinct banks),
-// constants by 4-byte copies (any alignment).
-constexpr int kC4Warps = 8, kC4Ring = 5, kC4Tiles = 4;
-constexpr int kC4CodeBytes = 16 * 128, kC4ScaleBytes = 16 * 4 * 4;
+// CTA pair owns a run of row tiles; its 16 warps each have their own share of the contraction, and their sums meet
+// at the end of a pass of 4 tiles. Codes and constants of two tiles and 256 elements come by TMA into two slots
+// per warp (32 rows x 128 bytes, 128-byte swizzle; quad g takes row 2 (g % 4) + g / 4 of each 8, whose 8-byte
+// loads then hit distinct banks). (Boxes of 16 rows x 64 or 128 bytes with 4-byte copies of the constants took
+// 51 us for 16 tokens through 8192 x 22016, 32 us of it for the stream alone.)
+constexpr int kC4Warps = 8, kC4Tiles = 4;
+constexpr int kC4CodeBytes = 32 * 128, kC4ScaleBytes = 32 * 4 * 4;
 constexpr uint32_t kC4Slots = 2u << 16;
-constexpr uint32_t kC4Scales = kC4Slots + kC4Warps * kC4Ring * kC4CodeBytes;
-constexpr uint32_t kC4Bars = kC4Scales + kC4Warps * kC4Ring * kC4ScaleBytes;
-constexpr int kC4Smem = static_cast<int>(kC4Bars) + kC4Warps * kC4Ring * 8;
+constexpr uint32_t kC4Scales = kC4Slots + kC4Warps * 2 * kC4CodeBytes;
+constexpr uint32_t kC4Bars = kC4Scales + kC4Warps * 2 * kC4ScaleBytes;
+constexpr int kC4Smem = static_cast<int>(kC4Bars) + kC4Warps * 2 * 8;
 __host__ __device__ constexpr int c4_peer_bytes(int NT) { return kC4Tiles * 16 * 8 * NT * 4; }
 static_assert(kC4Smem <= 227 * 1024 && kClBaseMax + (kC4Warps + 1) * c4_peer_bytes(2) <= 65536, "shared memory");
 
-template <int NT>
+// VEC: constants by TMA (K % 256 == 0), else by 4-byte copies.
+template <int NT, bool VEC>
 __global__ void __launch_bounds__(kC4Warps * 32, 1) __cluster_dims__(2, 1, 1)
-    codebook_linear4_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ ClParams p,
+    codebook_linear4_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmS, const __grid_constant__ ClParams p,
                             const __grid_constant__ CodebookArg cb) {
-  constexpr int TT = 8 * NT, R = kC4Ring;
+  constexpr int TT = 8 * NT;
   extern __shared__ __align__(1024) uint8_t cl_smem[];
   const uint32_t base = smem_u32(cl_smem), window = base & 0xFF000000u;
   const uint32_t table = window | kClTable;
@@ -484,12 +486,13 @@ __global__ void __launch_bounds__(kC4Warps * 32, 1) __cluster_dims__(2, 1, 1)
     if (threadIdx.x == 0) raise_status(kStatusTimeout);
     return;
   }
-  const uint32_t slots = (window | kC4Slots) + warp * R * kC4CodeBytes;
-  const uint32_t scales = window + kC4Scales + warp * R * kC4ScaleBytes;
-  const uint32_t bars = window + kC4Bars + warp * R * 8;
+  const uint32_t slots = (window | kC4Slots) + warp * 2 * kC4CodeBytes;
+  const uint32_t scales = window + kC4Scales + warp * 2 * kC4ScaleBytes;
+  const uint32_t bars = window + kC4Bars + warp * 2 * 8;
   const uint32_t red = base + c4_peer_bytes(NT);     // the warps' sums; the pair's second half hands over at base
   if (lane == 0) {
-    for (int s = 0; s < R; ++s) asm volatile("mbarrier.init.shared::cta.b64 [%0], 33;" ::"r"(bars + 8 * s));
+    for (int s = 0; s < 2; ++s)
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bars + 8 * s), "r"(VEC ? 1 : 33));
     fence_barrier_init();
   }
   for (int i = threadIdx.x; i < 256 * 32; i += blockDim.x) {
@@ -504,33 +507,36 @@ __global__ void __launch_bounds__(kC4Warps * 32, 1) __cluster_dims__(2, 1, 1)
   const int t_lo = static_cast<int>(static_cast<int64_t>(pair) * p.tiles / p.pairs);
   const int t_hi = static_cast<int>(static_cast<int64_t>(pair + 1) * p.tiles / p.pairs);
   const int part = rank * kC4Warps + warp;           // this warp's share of the blocks
-  const int k_lo = static_cast<int>(static_cast<int64_t>(part) * p.nkb / (2 * kC4Warps));
-  const int k_hi = static_cast<int>(static_cast<int64_t>(part + 1) * p.nkb / (2 * kC4Warps));
-  const int nu = (k_hi - k_lo + 3) / 4;
+  const int units = (p.nkb + 3) / 4;                 // of 256 elements
+  const int u_lo = part * units / (2 * kC4Warps), nu = (part + 1) * units / (2 * kC4Warps) - u_lo;
   uint32_t in_slot = 0, slot = 0, phase = 0;
   bool ok = true;
   for (int t0 = t_lo; t0 < t_hi; t0 += kC4Tiles) {
-    const int nt = min(kC4Tiles, t_hi - t0), n = nu * nt;
-    int issued = 0, done = 0, fk = k_lo, ft = 0;     // the unit to fetch next: block fk, tile ft
+    const int nt = min(kC4Tiles, t_hi - t0), halves = (nt + 1) / 2, n = nu * halves;
+    int issued = 0, done = 0, fu = u_lo, fh = 0;     // what to fetch next: unit fu, tiles 2 fh and 2 fh + 1
     auto fetch = [&]() {
       const uint32_t bar = bars + 8 * in_slot, sdst = scales + in_slot * kC4ScaleBytes;
-      const int row = (t0 + ft) * 16;
+      const int row = (t0 + 2 * fh) * 16;
+      if constexpr (!VEC) {
 #pragma unroll
-      for (int e = lane; e < 64; e += 32) {
-        const int r = row + (e >> 2), kb = fk + (e & 3);
-        const bool in = r < p.N && kb < k_hi;        // blocks of the next warp's share: a constant of 0
-        c1_cp4(sdst + 4u * e, p.absmax + (in ? static_cast<int64_t>(r) * p.nkb + kb : 0), in ? 4u : 0u);
+        for (int e = lane; e < 128; e += 32) {
+          const int r = row + (e >> 2), kb = 4 * fu + (e & 3);
+          const bool in = r < p.N && kb < p.nkb;
+          c1_cp4(sdst + 4u * e, p.absmax + (in ? static_cast<int64_t>(r) * p.nkb + kb : 0), in ? 4u : 0u);
+        }
+        c1_cp_arrive(bar);
       }
-      c1_cp_arrive(bar);
       if (lane == 0) {
-        c1_expect(bar, kC4CodeBytes);
-        c1_tma(slots + in_slot * kC4CodeBytes, &tmC, bar, fk * 32, row);
+        c1_expect(bar, kC4CodeBytes + (VEC ? kC4ScaleBytes : 0));
+        c1_tma(slots + in_slot * kC4CodeBytes, &tmC, bar, fu * 128, row);
+        if constexpr (VEC) c1_tma(sdst, &tmS, bar, fu * 4, row);
       }
-      in_slot = in_slot + 1 == R ? 0 : in_slot + 1;
+      in_slot ^= 1;
       ++issued;
-      if (++ft == nt) { ft = 0; fk += 4; }
+      if (++fh == halves) { fh = 0; ++fu; }
     };
-    for (int s = 0; s < R && s < n; ++s) fetch();
+    if (n > 0) fetch();
+    if (n > 1) fetch();
     float acc[kC4Tiles][NT][4] = {};
     for (int u = 0; u < nu && ok; ++u) {
       uint4 x[4][NT][2];
@@ -539,8 +545,8 @@ __global__ void __launch_bounds__(kC4Warps * 32, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
         for (int m = 0; m < NT; ++m) {
           x[b][m][0] = x[b][m][1] = make_uint4(0, 0, 0, 0);
-          const int kb = k_lo + 4 * u + b;
-          if (8 * m + g < p.T && kb < k_hi) {
+          const int kb = 4 * (u_lo + u) + b;
+          if (8 * m + g < p.T && kb < p.nkb) {
             const uint4* xp = reinterpret_cast<const uint4*>(p.X + (static_cast<int64_t>(8 * m + g) * p.nkb + kb) * 64 + 16 * j);
             x[b][m][0] = __ldg(xp);
             x[b][m][1] = __ldg(xp + 1);
@@ -549,9 +555,9 @@ __global__ void __launch_bounds__(kC4Warps * 32, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
       for (int t = 0; t < kC4Tiles; ++t) {
         if (t >= nt || !ok) break;
-        if (!__all_sync(0xffffffffu, mbar_wait_addr(bars + 8 * slot, phase))) { ok = false; break; }
-        const uint32_t at = slots + slot * kC4CodeBytes + 128u * gr + 8u * (j & 1);
-        const uint32_t sa = scales + slot * kC4ScaleBytes + 16u * gr;
+        if (t % 2 == 0 && !__all_sync(0xffffffffu, mbar_wait_addr(bars + 8 * slot, phase))) { ok = false; break; }
+        const uint32_t at = slots + slot * kC4CodeBytes + 2048u * (t & 1) + 128u * gr + 8u * (j & 1);
+        const uint32_t sa = scales + slot * kC4ScaleBytes + 256u * (t & 1) + 16u * gr;
         uint2 w[4][2];
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
@@ -560,11 +566,13 @@ __global__ void __launch_bounds__(kC4Warps * 32, 1) __cluster_dims__(2, 1, 1)
           w[b][1] = dc_ld64(c + 1024);
         }
         const uint4 f0 = dc_ld128(sa), f1 = dc_ld128(sa + 128);
-        __syncwarp();                                // the slot has been read
-        slot = slot + 1 == R ? 0 : slot + 1;
-        phase ^= slot == 0 ? 1u : 0u;
-        ++done;
-        if (issued < n) fetch();
+        if (t % 2 == 1 || t == nt - 1) {
+          __syncwarp();                              // the slot has been read
+          slot ^= 1;
+          phase ^= slot ^ 1;
+          ++done;
+          if (issued < n) fetch();
+        }
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
           const uint2 u0 = w[b][0], u1 = w[b][1];
@@ -595,8 +603,8 @@ __global__ void __launch_bounds__(kC4Warps * 32, 1) __cluster_dims__(2, 1, 1)
     }
     for (; done < issued; ++done) {                  // after a wait that gave up: this warp's copies in flight
       mbar_wait_short_addr(bars + 8 * slot, phase);
-      slot = slot + 1 == R ? 0 : slot + 1;
-      phase ^= slot == 0 ? 1u : 0u;
+      slot ^= 1;
+      phase ^= slot ^ 1;
     }
 #pragma unroll
     for (int t = 0; t < kC4Tiles; ++t)
