@@ -916,15 +916,18 @@ int launch_rope_type(RopeParams& p, bool half, bool copy_tail, int64_t step, int
 }
 
 // ---- vocabulary loss -------------------------------------------------------------------------------
-constexpr int kVlCtas = 148;                              // one CTA per SM of a B200 (fixed: the plan sizes the workspace)
-constexpr int64_t kVlPieceWords = int64_t(1) << 26;       // token x word weights of one piece (bf16: 128 MB)
+constexpr int kVlSms = 148;                               // CTAs of a B200 (fixed: the plan sizes the workspace)
+constexpr int64_t kVlPieceWords = int64_t(1) << 26;       // row x word weights of one piece (bf16: 128 MB)
 constexpr int64_t kVlPieceRows = 16384;
 
 // How a call is cut up, from its sizes alone, and its workspace (each part 256-byte aligned).
 struct VlPlan {
-  int64_t rows, pitch;        // tokens per piece (a multiple of 128), words per row of the weights
-  int tiles_v, splits, kb_split;
-  size_t count, target, ly, loss, factor, stats, weights, part, total;
+  int64_t rows, pitch;        // rows per piece (a multiple of 128), words per row of the weights
+  bool pair;                  // CTA pairs, 256 rows a tile
+  int workers;                // CTAs, or pairs of them
+  int bn;                     // words per tile of the logits
+  int gw;                     // workers of the gradient's product
+  size_t count, token, target, ly, loss, packed, stats, factor, weights, part, total;
 };
 VlPlan vl_plan(int64_t T, int64_t V, int64_t K, bool grad) {
   VlPlan w{};
@@ -932,33 +935,43 @@ VlPlan vl_plan(int64_t T, int64_t V, int64_t K, bool grad) {
   int64_t most = kVlPieceRows;
   if (grad) most = std::min(most, std::max<int64_t>(kVlM, kVlPieceWords / w.pitch / kVlM * kVlM));
   w.rows = cdiv(cdiv(T, cdiv(T, most)), kVlM) * kVlM;
-  w.tiles_v = static_cast<int>(cdiv(V, kVlN));
-  // the gradient's tiles, split along the vocabulary while they do not fill one wave (at least 8 steps each)
-  const int64_t tiles = w.rows / kVlM * cdiv(K, kVlN), nkb = cdiv(V, kVlK);
-  const int64_t s = std::max<int64_t>(1, std::min(kVlCtas / tiles, nkb / 8));
-  w.kb_split = static_cast<int>(cdiv(nkb, s));
-  w.splits = static_cast<int>(cdiv(nkb, w.kb_split));
+  w.pair = w.rows > kVlM;
+  w.workers = w.pair ? kVlSms / 2 : kVlSms;
+  const int mt = w.pair ? 2 * kVlM : kVlM;
+  // Logits tiles are as wide as fills whole waves best: waves x (width + 16 for a tile's own overhead). 32000
+  // words for one row tile are 125 tiles of 256, which leave 23 SMs idle, or 143 of 224.
+  int64_t best = INT64_MAX;
+  for (int bn = kVlN; bn >= 128; bn -= 32) {
+    const int64_t cost = cdiv(cdiv(w.rows, mt) * cdiv(V, bn), w.workers) * (bn + 16);
+    if (cost < best) { best = cost; w.bn = bn; }
+  }
+  // at least 4 contraction steps of the gradient's product per worker
+  w.gw = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(w.workers, cdiv(w.rows, mt) * cdiv(K, kVlN) * cdiv(V, kVlK) / 4)));
   size_t at = 0;
   auto take = [&](size_t bytes) { const size_t p = at; at += align256(bytes); return p; };
-  w.count = take(8);
-  w.target = take(static_cast<size_t>(T) * 8);
-  w.ly = take(static_cast<size_t>(T) * 4);
+  w.count = take(4);
+  w.token = take(static_cast<size_t>(T) * 4);
+  w.target = take(static_cast<size_t>(T) * 4);
   w.loss = take(static_cast<size_t>(T) * 4);
-  w.stats = take(static_cast<size_t>(w.tiles_v) * w.rows * sizeof(float2));
+  w.ly = take(static_cast<size_t>(w.rows) * 4);
+  w.packed = take(static_cast<size_t>(w.rows) * K * 2);
+  w.stats = take(static_cast<size_t>(cdiv(V, w.bn)) * w.rows * sizeof(float2));
   if (grad) {
     w.factor = take(static_cast<size_t>(w.rows) * 4);
     w.weights = take(static_cast<size_t>(w.rows) * w.pitch * 2);
-    if (w.splits > 1) w.part = take(static_cast<size_t>(w.splits) * w.rows * K * 4);
+    w.part = take(static_cast<size_t>(w.gw) * 2 * mt * kVlN * 4);
   }
   w.total = at;
   return w;
 }
 template <bool GRAD>
-int launch_vl_gemm(const CUtensorMap& a, const CUtensorMap& b, const VlParams& p, int sms, cudaStream_t st) {
-  auto kern = vl_gemm_kernel<GRAD>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kVlSmemBytes) != cudaSuccess)
+int launch_vl_gemm(bool pair, int workers, const CUtensorMap& a, const CUtensorMap& a2, const CUtensorMap& b,
+                   const VlParams& p, cudaStream_t st) {
+  const int smem = pair ? VlCfg<true>::SMEM_BYTES : VlCfg<false>::SMEM_BYTES;
+  auto kern = pair ? vl_gemm2_kernel<GRAD> : vl_gemm1_kernel<GRAD>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return cuda_fail(cudaGetLastError(), "cudaFuncSetAttribute", __LINE__);
-  kern<<<std::min(p.tiles_m * p.tiles_n * p.splits, sms), kVlThreads, kVlSmemBytes, st>>>(a, b, p);
+  kern<<<workers * (pair ? 2 : 1), kVlThreads, smem, st>>>(a, a2, b, p);
   return launched();
 }
 bool vl_shape_ok(int64_t T, int64_t V, int64_t K) {
@@ -968,70 +981,76 @@ bool vl_shape_ok(int64_t T, int64_t V, int64_t K) {
 int run_vocab_loss(const __nv_bfloat16* X, int64_t T, const __nv_bfloat16* W, int64_t V, int64_t K, const void* targets,
                    bool t64, int64_t ignore, int reduction, const float* dloss, float* loss, float* total,
                    __nv_bfloat16* dX, char* ws, cudaStream_t st) {
-  int sms = 0;
-  if (int e = check_device(&sms)) return e;
+  if (int e = check_device(nullptr)) return e;
   const VlPlan L = vl_plan(T, V, K, dX != nullptr);
-  auto* count = reinterpret_cast<unsigned long long*>(ws + L.count);
-  auto* target = reinterpret_cast<int64_t*>(ws + L.target);
-  auto* ly = reinterpret_cast<float*>(ws + L.ly);
+  int* count = reinterpret_cast<int*>(ws + L.count);
+  int* token = reinterpret_cast<int*>(ws + L.token);
+  int* target = reinterpret_cast<int*>(ws + L.target);
   float* tok_loss = loss ? loss : reinterpret_cast<float*>(ws + L.loss);
+  float* ly = reinterpret_cast<float*>(ws + L.ly);
+  auto* packed = reinterpret_cast<__nv_bfloat16*>(ws + L.packed);
   auto* stats = reinterpret_cast<float2*>(ws + L.stats);
   auto* weights = dX ? reinterpret_cast<__nv_bfloat16*>(ws + L.weights) : nullptr;
   float* factor = dX ? reinterpret_cast<float*>(ws + L.factor) : nullptr;
   const int mean = reduction == QLORA_LOSS_MEAN ? 1 : 0;
-  if (cudaMemsetAsync(count, 0, 8, st) != cudaSuccess) return cuda_fail(cudaGetLastError(), "cudaMemsetAsync", __LINE__);
-  const unsigned tg = static_cast<unsigned>(cdiv(T, 8));
+  const int rows = static_cast<int>(L.rows), mt = L.pair ? 2 * kVlM : kVlM;
   if (t64)
-    vl_target_kernel<int64_t><<<tg, 256, 0, st>>>(X, W, static_cast<const int64_t*>(targets), T, V, static_cast<int>(K),
-                                                  ignore, target, ly, count);
+    vl_index_kernel<int64_t><<<1, 1024, 0, st>>>(static_cast<const int64_t*>(targets), static_cast<int>(T), V, ignore, token,
+                                                 target, tok_loss, count);
   else
-    vl_target_kernel<int32_t><<<tg, 256, 0, st>>>(X, W, static_cast<const int32_t*>(targets), T, V, static_cast<int>(K),
-                                                  ignore, target, ly, count);
+    vl_index_kernel<int32_t><<<1, 1024, 0, st>>>(static_cast<const int32_t*>(targets), static_cast<int>(T), V, ignore, token,
+                                                 target, tok_loss, count);
   if (int e = launched()) return e;
-  CUtensorMap tw, tx, twm, tp;
-  if (!tmap_kmajor(&tw, W, K, V, kVlN)) return cuda_fail(cudaGetLastError(), "tensor-map encode", __LINE__);
-  if (dX && !tmap_mnmajor(&twm, W, K, V)) return cuda_fail(cudaGetLastError(), "tensor-map encode", __LINE__);
-  for (int64_t r0 = 0; r0 < T; r0 += L.rows) {
-    const int64_t rows = std::min(L.rows, T - r0);
-    if (!tmap_kmajor(&tx, X + r0 * K, K, rows, kVlM)) return cuda_fail(cudaGetLastError(), "tensor-map encode", __LINE__);
+  const int tiles_v = static_cast<int>(cdiv(V, L.bn)), ctas = L.pair ? 2 : 1;
+  CUtensorMap tw, tpk, twm = {}, tp = {};
+  if (!tmap_kmajor(&tw, W, K, V, L.bn / ctas) || !tmap_kmajor(&tpk, packed, K, rows, kVlM) ||
+      (dX && (!tmap_mnmajor(&twm, W, K, V) ||
+              !make_tmap_t(&tp, weights, TmType::kBf16, V, rows, L.pitch, kVlK, kVlM, true))))
+    return cuda_fail(cudaGetLastError(), "tensor-map encode", __LINE__);
+  for (int64_t r0 = 0; r0 < T; r0 += rows) {
+    CUtensorMap tx;
+    const int here = static_cast<int>(std::min<int64_t>(rows, T - r0));       // rows of this piece, at most
+    if (!tmap_kmajor(&tx, X + r0 * K, K, here, kVlM)) return cuda_fail(cudaGetLastError(), "tensor-map encode", __LINE__);
+    const int64_t warps = here + (dX && r0 == 0 ? T : 0);
+    vl_target_kernel<<<static_cast<unsigned>(cdiv(warps, 8)), 256, 0, st>>>(
+        X, W, static_cast<int>(K), static_cast<int>(r0), here, static_cast<int>(T), count, token, target, ly, packed,
+        r0 == 0 ? dX : nullptr);
+    if (int e = launched()) return e;
     VlParams p{};
-    p.rows = static_cast<int>(rows);
+    p.count = count;
+    p.r0 = static_cast<int>(r0);
+    p.rows_max = here;
+    p.copied = static_cast<int>(T);
     p.cols = static_cast<int>(V);
-    p.tiles_m = static_cast<int>(cdiv(rows, kVlM));
-    p.tiles_n = L.tiles_v;
-    p.splits = 1;
-    p.nkb = p.kb_split = static_cast<int>(cdiv(K, kVlK));
+    p.bn = L.bn;
+    p.tiles_n = tiles_v;
+    p.nkb = static_cast<int>(cdiv(K, kVlK));
     p.target = target + r0;
-    p.ly = ly + r0;
+    p.ly = ly;
     p.stats = stats;
     p.weights = weights;
     p.pitch = L.pitch;
-    if (int e = launch_vl_gemm<false>(tx, tw, p, sms, st)) return e;
-    vl_finish_kernel<<<static_cast<unsigned>(cdiv(rows, 8)), 256, 0, st>>>(
-        stats, static_cast<int>(rows), L.tiles_v, target + r0, static_cast<int>(V), dloss ? dloss + r0 : nullptr, mean,
-        count, tok_loss + r0, weights, L.pitch, factor);
+    const int64_t tiles = cdiv(here, mt) * tiles_v;
+    if (int e = launch_vl_gemm<false>(L.pair, static_cast<int>(std::min<int64_t>(tiles, L.workers)), tx, tpk, tw, p, st)) return e;
+    vl_finish_kernel<<<static_cast<unsigned>(cdiv(here, 8)), 256, 0, st>>>(
+        stats, static_cast<int>(r0), here, tiles_v, L.bn, count, token, target, static_cast<int>(V), dloss, mean, tok_loss,
+        weights, L.pitch, factor);
     if (int e = launched()) return e;
     if (!dX) continue;
-    if (!make_tmap_t(&tp, weights, TmType::kBf16, V, rows, L.pitch, kVlK, kVlM, true))
-      return cuda_fail(cudaGetLastError(), "tensor-map encode", __LINE__);
-    VlParams d{};
-    d.rows = static_cast<int>(rows);
+    VlParams d = p;
     d.cols = static_cast<int>(K);
-    d.tiles_m = p.tiles_m;
+    d.bn = kVlN;
     d.tiles_n = static_cast<int>(cdiv(K, kVlN));
-    d.splits = L.splits;
     d.nkb = static_cast<int>(cdiv(V, kVlK));
-    d.kb_split = L.kb_split;
+    d.token = token + r0;
     d.factor = factor;
-    d.out = dX + r0 * K;
+    d.out = dX;
     d.part = reinterpret_cast<float*>(ws + L.part);
-    if (int e = launch_vl_gemm<true>(tp, twm, d, sms, st)) return e;
-    if (L.splits > 1) {
-      const unsigned grid = static_cast<unsigned>(std::min<int64_t>(cdiv(rows * K / 4, 256), int64_t(sms) * 8));
-      vl_reduce_kernel<<<grid, 256, 0, st>>>(reinterpret_cast<const float4*>(d.part), L.splits, rows, K / 4, factor,
-                                             reinterpret_cast<uint2*>(d.out));
-      if (int e = launched()) return e;
-    }
+    if (int e = launch_vl_gemm<true>(L.pair, L.gw, tp, tp, twm, d, st)) return e;
+    const dim3 rg(static_cast<unsigned>(cdiv(here, mt) * d.tiles_n), static_cast<unsigned>(mt / 16));
+    if (L.pair) vl_reduce_kernel<2><<<rg, 256, 0, st>>>(d.part, d, L.gw);
+    else vl_reduce_kernel<1><<<rg, 256, 0, st>>>(d.part, d, L.gw);
+    if (int e = launched()) return e;
   }
   if (total) {
     vl_total_kernel<<<1, 1024, 0, st>>>(tok_loss, T, mean, count, total);
