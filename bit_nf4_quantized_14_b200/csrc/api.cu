@@ -926,7 +926,6 @@ struct VlPlan {
   bool pair;                  // CTA pairs, 256 rows a tile
   int workers;                // CTAs, or pairs of them
   int bn;                     // words per tile of the logits
-  int gw;                     // workers of the gradient's product
   size_t count, token, target, ly, loss, packed, stats, factor, weights, part, total;
 };
 VlPlan vl_plan(int64_t T, int64_t V, int64_t K, bool grad) {
@@ -945,8 +944,6 @@ VlPlan vl_plan(int64_t T, int64_t V, int64_t K, bool grad) {
     const int64_t cost = cdiv(cdiv(w.rows, mt) * cdiv(V, bn), w.workers) * (bn + 16);
     if (cost < best) { best = cost; w.bn = bn; }
   }
-  // at least 4 contraction steps of the gradient's product per worker
-  w.gw = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(w.workers, cdiv(w.rows, mt) * cdiv(K, kVlN) * cdiv(V, kVlK) / 4)));
   size_t at = 0;
   auto take = [&](size_t bytes) { const size_t p = at; at += align256(bytes); return p; };
   w.count = take(4);
@@ -959,7 +956,7 @@ VlPlan vl_plan(int64_t T, int64_t V, int64_t K, bool grad) {
   if (grad) {
     w.factor = take(static_cast<size_t>(w.rows) * 4);
     w.weights = take(static_cast<size_t>(w.rows) * w.pitch * 2);
-    w.part = take(static_cast<size_t>(w.gw) * 2 * mt * kVlN * 4);
+    w.part = take(static_cast<size_t>(kVlParts) * w.workers * mt * kVlN * 4);
   }
   w.total = at;
   return w;
@@ -1046,10 +1043,10 @@ int run_vocab_loss(const __nv_bfloat16* X, int64_t T, const __nv_bfloat16* W, in
     d.factor = factor;
     d.out = dX;
     d.part = reinterpret_cast<float*>(ws + L.part);
-    if (int e = launch_vl_gemm<true>(L.pair, L.gw, tp, tp, twm, d, st)) return e;
-    const dim3 rg(static_cast<unsigned>(cdiv(here, mt) * d.tiles_n), static_cast<unsigned>(mt / 16));
-    if (L.pair) vl_reduce_kernel<2><<<rg, 256, 0, st>>>(d.part, d, L.gw);
-    else vl_reduce_kernel<1><<<rg, 256, 0, st>>>(d.part, d, L.gw);
+    if (int e = launch_vl_gemm<true>(L.pair, L.workers, tp, tp, twm, d, st)) return e;
+    const dim3 rg(static_cast<unsigned>(L.workers), static_cast<unsigned>(mt / 16));
+    if (L.pair) vl_reduce_kernel<2><<<rg, 256, 0, st>>>(d, L.workers);
+    else vl_reduce_kernel<1><<<rg, 256, 0, st>>>(d, L.workers);
     if (int e = launched()) return e;
   }
   if (total) {

@@ -20,9 +20,11 @@
 //   vl_finish   one warp per row: adds the tiles' sums in order, loss, the weight -Z of the target, the row's
 //               factor g / (1 + Z); brings a row whose tiles have shifts to one shift;
 //   vl_gemm<1>  dX = weights x W (contraction over the vocabulary, W as the MN-major operand), times the row's
-//               factor in fp32, rounded once to bf16. The contraction steps of all tiles are one run cut evenly over
-//               the CTA pairs (2048 x 4096 outputs are 128 tiles for 74 pairs); a tile that two or more of them
-//               share leaves fp32 partial sums that vl_reduce adds in order.
+//               factor in fp32, rounded once to bf16. Whole waves of tiles run in step along the vocabulary, so W
+//               and the weights pass through L2 once; the tiles of a last, partly filled wave are cut along the
+//               vocabulary to fill the CTA pairs (2048 x 4096 outputs are 128 tiles for 74 pairs) and leave fp32
+//               partial sums that vl_reduce adds in order. (One run of all tiles' steps cut evenly over the pairs
+//               filled them too, but every pair read another part of W: 487 against 428 us uncut.)
 // The tensor pipe bounds it: 2 T V K FLOP for the loss, 4 T V K with the gradient (kept weights, no second
 // logits product). All sums are in a fixed order: results are deterministic.
 //
@@ -66,15 +68,28 @@ struct VlParams {
   const int* token;             // <1>: the token of each row
   const float* factor;          // <1>: per row
   __nv_bfloat16* out;           // <1>: [token][cols]
-  float* part;                  // <1>: per pair (or CTA) two partial tiles of [128 CTAS][256]
+  float* part;                  // <1>: partial tiles of [128 CTAS][256]
 };
 __device__ __forceinline__ int vl_rows(const int* count, int r0, int rows_max) {
   return max(0, min(rows_max, *count - r0));
 }
-// The run of contraction steps of a split over G workers: worker c has steps [lo(c), lo(c + 1)).
-__device__ __forceinline__ int64_t vl_lo(int64_t steps, int c, int G) { return steps * c / G; }
-__device__ __forceinline__ int vl_owner(int64_t steps, int64_t pos, int G) {
-  return static_cast<int>(((pos + 1) * G - 1) / steps);
+// How the gradient's tiles are dealt to its workers: `full` whole ones in full waves, then the others in `cuts`
+// parts of the contraction each. The number of cuts minimises what the last wave takes, counted in contraction
+// steps, a part's write and read of its fp32 tile as a quarter of a step; at most kVlParts parts per worker.
+constexpr int kVlParts = 3;
+struct VlDeal { int full, rest, cuts; };
+__host__ __device__ __forceinline__ VlDeal vl_deal(int tiles, int workers, int nkb) {
+  VlDeal d;
+  d.full = tiles / workers * workers;
+  d.rest = tiles - d.full;
+  d.cuts = 1;
+  float best = 1e30f;
+  for (int s = 1; s <= 32 && d.rest * s <= kVlParts * workers && s * 4 <= nkb + 3; ++s) {
+    const int waves = (d.rest * s + workers - 1) / workers;
+    const float cost = static_cast<float>(waves) * nkb / s + (s > 1 ? 0.25f * d.rest * s : 0.0f);
+    if (cost < best) { best = cost; d.cuts = s; }
+  }
+  return d;
 }
 
 __device__ __forceinline__ uint32_t vl_peer(uint32_t addr, uint32_t rank) {    // the same address in CTA `rank` of the pair
@@ -165,29 +180,34 @@ __device__ __forceinline__ void vl_gemm(const CUtensorMap& tmA, const CUtensorMa
 
   const int rows = vl_rows(p.count, p.r0, p.rows_max);
   const int tiles_m = (rows + kVlM * C::CTAS - 1) / (kVlM * C::CTAS);
-  // work: <0> whole tiles, dealt out in turn; <1> the run of all tiles' contraction steps, cut evenly
-  const int64_t steps = static_cast<int64_t>(tiles_m) * p.tiles_n * (GRAD ? p.nkb : 1);
-  const int64_t lo = GRAD ? vl_lo(steps, worker, workers) : worker, hi = GRAD ? vl_lo(steps, worker + 1, workers) : steps;
+  const int tiles = tiles_m * p.tiles_n;
+  const VlDeal deal = GRAD ? vl_deal(tiles, workers, p.nkb) : VlDeal{tiles, 0, 1};
+  const int num_items = deal.full + deal.rest * deal.cuts;
   const int bn_cta = p.bn / C::CTAS;
   struct Item { int m0, n0, kb0, kb1; };
-  auto item = [&](int64_t pos) {
+  auto item = [&](int i) {
     Item t;
-    const int64_t tile = GRAD ? pos / p.nkb : pos;
-    t.m0 = static_cast<int>(tile % tiles_m) * kVlM * C::CTAS;
-    t.n0 = static_cast<int>(tile / tiles_m) * p.bn;
-    t.kb0 = GRAD ? static_cast<int>(pos - tile * p.nkb) : 0;
-    t.kb1 = GRAD ? static_cast<int>(min(static_cast<int64_t>(p.nkb), t.kb0 + (hi - pos))) : p.nkb;
+    int tile = i;
+    t.kb0 = 0;
+    t.kb1 = p.nkb;
+    if (GRAD && i >= deal.full) {
+      const int cut = (i - deal.full) / deal.rest;
+      tile = deal.full + (i - deal.full) % deal.rest;
+      t.kb0 = static_cast<int>(static_cast<int64_t>(p.nkb) * cut / deal.cuts);
+      t.kb1 = static_cast<int>(static_cast<int64_t>(p.nkb) * (cut + 1) / deal.cuts);
+    }
+    t.m0 = (tile % tiles_m) * kVlM * C::CTAS;
+    t.n0 = (tile / tiles_m) * p.bn;
     return t;
   };
-  auto next = [&](int64_t pos, const Item& t) { return GRAD ? pos + (t.kb1 - t.kb0) : pos + workers; };
 
   if (warp == 0) {
     // ------------------------------- TMA producer (both CTAs) -------------------------------
     if (lane == 0) {
       const CUtensorMap* ma = !GRAD && *p.count < p.copied ? &tmA2 : &tmA;
       int it = 0;
-      for (int64_t pos = lo; pos < hi && !*abort_flag;) {
-        const Item t = item(pos);
+      for (int i = worker; i < num_items && !*abort_flag; i += workers) {
+        const Item t = item(i);
         for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
           const int s = it % ST, r = it / ST;
           if (it >= ST && !mbar_wait(&empty[s], (r - 1) & 1)) { *abort_flag = 1; break; }
@@ -206,7 +226,6 @@ __device__ __forceinline__ void vl_gemm(const CUtensorMap& tmA, const CUtensorMa
           }
           issued = it + 1;
         }
-        pos = next(pos, t);
       }
     }
   } else if (warp == 1) {
@@ -214,8 +233,8 @@ __device__ __forceinline__ void vl_gemm(const CUtensorMap& tmA, const CUtensorMa
     if (lane == 0 && rank == 0) {
       int it = 0, lt = 0;
       bool ok = true;
-      for (int64_t pos = lo; pos < hi && ok; ++lt) {
-        const Item t = item(pos);
+      for (int i = worker; i < num_items && ok; i += workers, ++lt) {
+        const Item t = item(i);
         const int b = lt & 1, u = lt >> 1;
         if (lt >= 2 && !mbar_wait(&tempty[b], (u - 1) & 1)) { ok = false; break; }
         tc_fence_after();
@@ -236,7 +255,6 @@ __device__ __forceinline__ void vl_gemm(const CUtensorMap& tmA, const CUtensorMa
         }
         if (!ok) break;
         vl_commit<PAIR>(&tfull[b]);
-        pos = next(pos, t);
       }
       if (!ok) *abort_flag = 1;
       vl_commit<PAIR>(drain);
@@ -246,8 +264,8 @@ __device__ __forceinline__ void vl_gemm(const CUtensorMap& tmA, const CUtensorMa
     const int q = warp & 3;
     const int tn = p.bn;
     int lt = 0;
-    for (int64_t pos = lo; pos < hi; ++lt) {
-      const Item t = item(pos);
+    for (int i = worker; i < num_items; i += workers, ++lt) {
+      const Item t = item(i);
       const int b = lt & 1, u = lt >> 1;
       const bool ok = mbar_wait(&tfull[b], u & 1);
       if (!__all_sync(0xffffffffu, ok && !*abort_flag)) { *abort_flag = 1; break; }
@@ -303,11 +321,10 @@ __device__ __forceinline__ void vl_gemm(const CUtensorMap& tmA, const CUtensorMa
         }
         if (live) p.stats[static_cast<int64_t>(t.n0 / tn) * p.rows_max + row] = make_float2(shift, sum);
       } else {
-        const bool whole = t.kb0 == 0 && t.kb1 == p.nkb;
+        const bool whole = i < deal.full || deal.cuts == 1;
         const float f = whole && live ? p.factor[row] : 0.0f;
         __nv_bfloat16* out = p.out + static_cast<int64_t>(whole && live ? p.token[row] : 0) * p.cols + t.n0;
-        // a worker's run begins inside a tile (its first partial) or ends inside one (its second)
-        float* part = p.part + (static_cast<int64_t>(2 * worker + (t.kb0 == 0 ? 1 : 0)) * kVlM * C::CTAS + in_tile) * kVlN;
+        float* part = whole ? nullptr : p.part + (static_cast<int64_t>(i - deal.full) * kVlM * C::CTAS + in_tile) * kVlN;
 #pragma unroll 1
         for (int c = 0; c < ncol; c += 16) {
           uint32_t v[16];
@@ -342,7 +359,6 @@ __device__ __forceinline__ void vl_gemm(const CUtensorMap& tmA, const CUtensorMa
         else
           mbar_arrive(&tempty[b]);
       }
-      pos = next(pos, t);
     }
   }
 
@@ -501,27 +517,25 @@ __global__ void __launch_bounds__(256) vl_finish_kernel(const float2* __restrict
   }
 }
 
-// The tiles of dX that more than one worker shares: their partial sums in order. One CTA per tile and 16 of its rows.
+// The tiles of dX that were cut: their partial sums in order. One CTA per tile and 16 of its rows.
 template <int CTAS>
-__global__ void __launch_bounds__(256) vl_reduce_kernel(const float* __restrict__ part, const __grid_constant__ VlParams p,
-                                                        int workers) {
+__global__ void __launch_bounds__(256) vl_reduce_kernel(const __grid_constant__ VlParams p, int workers) {
   constexpr int MT = kVlM * CTAS;
   const int rows = vl_rows(p.count, p.r0, p.rows_max);
   const int tiles_m = (rows + MT - 1) / MT;
-  const int64_t tiles = static_cast<int64_t>(tiles_m) * p.tiles_n, steps = tiles * p.nkb, tile = blockIdx.x;
-  if (tile >= tiles) return;
-  const int first = vl_owner(steps, tile * p.nkb, workers), last = vl_owner(steps, (tile + 1) * p.nkb - 1, workers);
-  if (first == last) return;
-  const int m0 = static_cast<int>(tile % tiles_m) * MT, n0 = static_cast<int>(tile / tiles_m) * p.bn;
+  const VlDeal deal = vl_deal(tiles_m * p.tiles_n, workers, p.nkb);
+  const int r = blockIdx.x, tile = deal.full + r;
+  if (deal.cuts == 1 || r >= deal.rest) return;
+  const int m0 = tile % tiles_m * MT, n0 = tile / tiles_m * p.bn;
   const int ncol = min(p.bn, p.cols - n0);
   for (int e = threadIdx.x; e < 16 * (kVlN / 8); e += blockDim.x) {
     const int in_tile = blockIdx.y * 16 + e / (kVlN / 8), row = m0 + in_tile, c = e % (kVlN / 8) * 8;
     if (row >= rows || c >= ncol) continue;
     float acc[8] = {};
-    for (int w = first; w <= last; ++w) {
-      if (vl_lo(steps, w, workers) == vl_lo(steps, w + 1, workers)) continue;      // fewer steps than workers
+#pragma unroll 4
+    for (int w = 0; w < deal.cuts; ++w) {
       const float4* src = reinterpret_cast<const float4*>(
-          part + (static_cast<int64_t>(2 * w + (w == first ? 1 : 0)) * MT + in_tile) * kVlN + c);
+          p.part + (static_cast<int64_t>(w * deal.rest + r) * MT + in_tile) * kVlN + c);
       const float4 a = src[0], b = src[1];
       acc[0] += a.x; acc[1] += a.y; acc[2] += a.z; acc[3] += a.w;
       acc[4] += b.x; acc[5] += b.y; acc[6] += b.z; acc[7] += b.w;
