@@ -167,7 +167,7 @@ bool make_codebook(const float* lv, int nl, CodebookArg* cb, BucketArg* bk) {
 // stream drains, and waits for it (griddepcontrol.wait) before touching its results.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl_smem(void (*kern)(KArgs...), dim3 grid, unsigned block, size_t smem, cudaStream_t st,
-                            Args... args) {
+                            const Args&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
@@ -952,7 +952,7 @@ VlPlan vl_plan(int64_t T, int64_t V, int64_t K, bool grad) {
   w.loss = take(static_cast<size_t>(T) * 4);
   w.ly = take(static_cast<size_t>(w.rows) * 4);
   w.packed = take(static_cast<size_t>(w.rows) * K * 2);
-  w.stats = take(static_cast<size_t>(cdiv(V, w.bn)) * w.rows * sizeof(float2));
+  w.stats = take(static_cast<size_t>(2 * cdiv(V, w.bn)) * w.rows * sizeof(float2));
   if (grad) {
     w.factor = take(static_cast<size_t>(w.rows) * 4);
     w.weights = take(static_cast<size_t>(w.rows) * w.pitch * 2);
@@ -961,6 +961,7 @@ VlPlan vl_plan(int64_t T, int64_t V, int64_t K, bool grad) {
   w.total = at;
   return w;
 }
+int vl_launched(cudaError_t e, int line) { return e == cudaSuccess ? launched() : cuda_fail(e, "cudaLaunchKernelEx", line); }
 template <bool GRAD>
 int launch_vl_gemm(bool pair, int workers, const CUtensorMap& a, const CUtensorMap& a2, const CUtensorMap& b,
                    const VlParams& p, cudaStream_t st) {
@@ -968,8 +969,7 @@ int launch_vl_gemm(bool pair, int workers, const CUtensorMap& a, const CUtensorM
   auto kern = pair ? vl_gemm2_kernel<GRAD> : vl_gemm1_kernel<GRAD>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return cuda_fail(cudaGetLastError(), "cudaFuncSetAttribute", __LINE__);
-  kern<<<workers * (pair ? 2 : 1), kVlThreads, smem, st>>>(a, a2, b, p);
-  return launched();
+  return vl_launched(launch_pdl_smem(kern, dim3(workers * (pair ? 2 : 1)), kVlThreads, smem, st, a, a2, b, p), __LINE__);
 }
 bool vl_shape_ok(int64_t T, int64_t V, int64_t K) {
   return T >= 1 && T <= kMaxTokens && V >= 1 && V < (int64_t(1) << 30) && K >= 8 && K <= (int64_t(1) << 20) &&
@@ -1008,11 +1008,11 @@ int run_vocab_loss(const __nv_bfloat16* X, int64_t T, const __nv_bfloat16* W, in
     CUtensorMap tx;
     const int here = static_cast<int>(std::min<int64_t>(rows, T - r0));       // rows of this piece, at most
     if (!tmap_kmajor(&tx, X + r0 * K, K, here, kVlM)) return cuda_fail(cudaGetLastError(), "tensor-map encode", __LINE__);
-    const int64_t warps = here + (dX && r0 == 0 ? T : 0);
-    vl_target_kernel<<<static_cast<unsigned>(cdiv(warps, 8)), 256, 0, st>>>(
-        X, W, static_cast<int>(K), static_cast<int>(r0), here, static_cast<int>(T), count, token, target, ly, packed,
-        r0 == 0 ? dX : nullptr);
-    if (int e = launched()) return e;
+    const int64_t blocks = here + (dX && r0 == 0 ? T : 0);
+    if (int e = vl_launched(launch_pdl_smem(vl_target_kernel, dim3(static_cast<unsigned>(blocks)), kVlRowThreads, 0, st, X, W,
+                                            static_cast<int>(K), static_cast<int>(r0), here, static_cast<int>(T), count, token,
+                                            target, ly, packed, r0 == 0 ? dX : nullptr), __LINE__))
+      return e;
     VlParams p{};
     p.count = count;
     p.r0 = static_cast<int>(r0);
@@ -1029,30 +1029,28 @@ int run_vocab_loss(const __nv_bfloat16* X, int64_t T, const __nv_bfloat16* W, in
     p.pitch = L.pitch;
     const int64_t tiles = cdiv(here, mt) * tiles_v;
     if (int e = launch_vl_gemm<false>(L.pair, static_cast<int>(std::min<int64_t>(tiles, L.workers)), tx, tpk, tw, p, st)) return e;
-    vl_finish_kernel<<<static_cast<unsigned>(cdiv(here, 8)), 256, 0, st>>>(
-        stats, static_cast<int>(r0), here, tiles_v, L.bn, count, token, target, static_cast<int>(V), dloss, mean, tok_loss,
-        weights, L.pitch, factor);
-    if (int e = launched()) return e;
+    if (int e = vl_launched(launch_pdl_smem(vl_finish_kernel, dim3(static_cast<unsigned>(cdiv(here, 32))), kVlFinishThreads, 0, st, stats,
+                                            static_cast<int>(r0), here, 2 * tiles_v, L.bn / 2, count, token, target, static_cast<int>(V),
+                                            dloss, mean, tok_loss, weights, L.pitch, factor), __LINE__))
+      return e;
     if (!dX) continue;
     VlParams d = p;
     d.cols = static_cast<int>(K);
-    d.bn = kVlN;
     d.tiles_n = static_cast<int>(cdiv(K, kVlN));
+    d.bn = static_cast<int>(cdiv(cdiv(K, d.tiles_n), 32) * 32);        // near-equal tiles
     d.nkb = static_cast<int>(cdiv(V, kVlK));
     d.token = token + r0;
     d.factor = factor;
     d.out = dX;
     d.part = reinterpret_cast<float*>(ws + L.part);
     if (int e = launch_vl_gemm<true>(L.pair, L.workers, tp, tp, twm, d, st)) return e;
-    const dim3 rg(static_cast<unsigned>(L.workers), static_cast<unsigned>(mt / 16));
-    if (L.pair) vl_reduce_kernel<2><<<rg, 256, 0, st>>>(d, L.workers);
-    else vl_reduce_kernel<1><<<rg, 256, 0, st>>>(d, L.workers);
-    if (int e = launched()) return e;
+    const dim3 rg(static_cast<unsigned>(L.workers), static_cast<unsigned>(mt / 8));
+    if (int e = vl_launched(launch_pdl_smem(L.pair ? vl_reduce_kernel<2> : vl_reduce_kernel<1>, rg, 256, 0, st, d, L.workers),
+                            __LINE__))
+      return e;
   }
-  if (total) {
-    vl_total_kernel<<<1, 1024, 0, st>>>(tok_loss, T, mean, count, total);
-    return launched();
-  }
+  if (total)
+    return vl_launched(launch_pdl_smem(vl_total_kernel, dim3(1), 1024, 0, st, tok_loss, T, mean, count, total), __LINE__);
   return QLORA_OK;
 }
 }  // namespace

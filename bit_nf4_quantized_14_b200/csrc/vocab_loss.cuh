@@ -10,14 +10,14 @@
 // buffer, 128 MB at most; the host launches for every token, the kernels read the count and stop at it):
 //   vl_index    numbers the tokens in the loss, in order; checks the targets;
 //   vl_target   l_y = X_t . W_y in fp32 on the CUDA cores (the tensor cores' fp32 accumulation truncates: over
-//               K = 8192 a logit of 12 came out 1e-4 low), one warp per row; copies the rows together where
+//               K = 8192 a logit of 12 came out 1e-4 low), one CTA per row; copies the rows together where
 //               tokens are left out, and zeroes those tokens' gradients;
 //   vl_gemm<0>  logits tile by tile on the tensor cores (a CTA pair: 256 rows x up to 256 words, K in steps of 64
 //               through a TMA-filled ring, two accumulators in tensor memory so the epilogue overlaps the next tile);
 //               epilogue: exp(d_v) rounded to bf16 (the MMA operand of the gradient; a relative 2^-8 of each weight
 //               at most) and its fp32 sum over the tile's words. Where a tile's largest d exceeds 40 its weights
 //               are stored relative to that d (a shift per row and tile), so nothing overflows;
-//   vl_finish   one warp per row: adds the tiles' sums in order, loss, the weight -Z of the target, the row's
+//   vl_finish   adds the tiles' sums in order, loss, the weight -Z of the target, the row's
 //               factor g / (1 + Z); brings a row whose tiles have shifts to one shift;
 //   vl_gemm<1>  dX = weights x W (contraction over the vocabulary, W as the MN-major operand), times the row's
 //               factor in fp32, rounded once to bf16. Whole waves of tiles run in step along the vocabulary, so W
@@ -41,16 +41,18 @@ namespace qnf4 {
 
 constexpr int kVlM = 128, kVlN = 256, kVlK = 64;      // rows per CTA; widest tile; contraction step
 constexpr int kVlABytes = kVlM * kVlK * 2;
+constexpr int kVlStore = 32 * 32 * 2;      // 32 rows x 32 weights on their way out
 template <bool PAIR> struct VlCfg {
   static constexpr int CTAS = PAIR ? 2 : 1;
   static constexpr int BROWS = kVlN / CTAS;           // words (or features) of a tile in one CTA's shared memory
   static constexpr int B_BYTES = BROWS * kVlK * 2;
   static constexpr int STAGE_BYTES = kVlABytes + B_BYTES;
   static constexpr int STAGES = PAIR ? 6 : 4;
-  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 256 + 1024;
+  static constexpr int STORE_BYTES = 8 * kVlStore;          // a buffer per epilogue warp
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + STORE_BYTES + 256 + 1024;
   static_assert(SMEM_BYTES <= 227 * 1024 && (2 * STAGES + 5) * 8 + 8 <= 256, "shared memory per CTA");
 };
-constexpr int kVlThreads = 6 * 32;
+constexpr int kVlThreads = 10 * 32;       // TMA, MMA, 8 epilogue warps
 constexpr float kVlMaxShift = 40.0f;      // exp(40) x any vocabulary stays far inside fp32 and bf16
 constexpr unsigned kStatusTarget = 4u;
 
@@ -62,7 +64,7 @@ struct VlParams {
   int tiles_n, nkb;             // column tiles; contraction blocks of 64
   const int* target;            // <0>: per row
   const float* ly;              // <0>: target logits
-  float2* stats;                // <0>: [column tile][rows_max] (shift, sum)
+  float2* stats;                // <0>: [half of a column tile][rows_max] (shift, sum)
   __nv_bfloat16* weights;       // <0>: [rows][pitch], or null (loss only)
   int64_t pitch;
   const int* token;             // <1>: the token of each row
@@ -78,17 +80,22 @@ __device__ __forceinline__ int vl_rows(const int* count, int r0, int rows_max) {
 // steps, a part's write and read of its fp32 tile as a quarter of a step; at most kVlParts parts per worker.
 constexpr int kVlParts = 3;
 struct VlDeal { int full, rest, cuts; };
-__host__ __device__ __forceinline__ VlDeal vl_deal(int tiles, int workers, int nkb) {
+__device__ __forceinline__ VlDeal vl_deal(int tiles, int workers, int nkb) {      // by a whole warp: a lane per cut
   VlDeal d;
   d.full = tiles / workers * workers;
   d.rest = tiles - d.full;
-  d.cuts = 1;
-  float best = 1e30f;
-  for (int s = 1; s <= 32 && d.rest * s <= kVlParts * workers && s * 4 <= nkb + 3; ++s) {
-    const int waves = (d.rest * s + workers - 1) / workers;
-    const float cost = static_cast<float>(waves) * nkb / s + (s > 1 ? 0.25f * d.rest * s : 0.0f);
-    if (cost < best) { best = cost; d.cuts = s; }
+  int cuts = static_cast<int>(threadIdx.x & 31) + 1;
+  float cost = 1e30f;
+  if (cuts == 1 || (d.rest * cuts <= kVlParts * workers && cuts * 4 <= nkb + 3))
+    cost = static_cast<float>((d.rest * cuts + workers - 1) / workers) * nkb / cuts +
+           (cuts > 1 ? 0.25f * d.rest * cuts : 0.0f);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float c = __shfl_xor_sync(0xffffffffu, cost, o);
+    const int s = __shfl_xor_sync(0xffffffffu, cuts, o);
+    if (c < cost || (c == cost && s < cuts)) { cost = c; cuts = s; }
   }
+  d.cuts = cuts;
   return d;
 }
 
@@ -132,6 +139,13 @@ __device__ __forceinline__ void vl_cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// Every kernel of a call but the first is launched to start while the one before it ends: it waits here, before it
+// touches anything that kernel wrote or reads, and lets the next one be set up in turn.
+__device__ __forceinline__ void vl_chain() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 template <bool GRAD, bool PAIR>
 __device__ __forceinline__ void vl_gemm(const CUtensorMap& tmA, const CUtensorMap& tmA2, const CUtensorMap& tmB,
                                         const VlParams& p) {
@@ -142,7 +156,8 @@ __device__ __forceinline__ void vl_gemm(const CUtensorMap& tmA, const CUtensorMa
   uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sA = base;
   uint8_t* sB = base + ST * kVlABytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(base + ST * C::STAGE_BYTES);
+  uint8_t* sE = base + ST * C::STAGE_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sE + C::STORE_BYTES);
   uint64_t* empty = full + ST;
   uint64_t* tfull = empty + ST;            // [2]
   uint64_t* tempty = tfull + 2;            // [2]
@@ -155,7 +170,7 @@ __device__ __forceinline__ void vl_gemm(const CUtensorMap& tmA, const CUtensorMa
   const int worker = PAIR ? blockIdx.x >> 1 : blockIdx.x, workers = PAIR ? gridDim.x >> 1 : gridDim.x;
   if (threadIdx.x == 0) {
     for (int s = 0; s < ST; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
-    for (int b = 0; b < 2; ++b) { mbar_init(&tfull[b], 1); mbar_init(&tempty[b], 4 * C::CTAS); }
+    for (int b = 0; b < 2; ++b) { mbar_init(&tfull[b], 1); mbar_init(&tempty[b], 8 * C::CTAS); }
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -174,6 +189,8 @@ __device__ __forceinline__ void vl_gemm(const CUtensorMap& tmA, const CUtensorMa
   __syncthreads();
   if constexpr (PAIR) vl_cluster_sync();
   tc_fence_after();
+  vl_chain();
+  asm volatile("fence.proxy.async;" ::: "memory");     // what earlier kernels stored, for this one's TMA
   const uint32_t tmem_base = *tmem_slot;
   const uint32_t idesc = idesc_bf16(kVlM * C::CTAS, 16, false, GRAD) - (2u << 17) + (static_cast<uint32_t>(p.bn >> 3) << 17);
   int issued = 0;
@@ -222,7 +239,7 @@ __device__ __forceinline__ void vl_gemm(const CUtensorMap& tmA, const CUtensorMa
           } else {
 #pragma unroll
             for (int a = 0; a < C::BROWS / 64; ++a)
-              vl_tma<PAIR>(sB + s * C::B_BYTES + a * 8192, &tmB, bar, t.n0 + rank * C::BROWS + 64 * a, kb * kVlK);
+              vl_tma<PAIR>(sB + s * C::B_BYTES + a * 8192, &tmB, bar, t.n0 + rank * bn_cta + 64 * a, kb * kVlK);
           }
           issued = it + 1;
         }
@@ -260,79 +277,125 @@ __device__ __forceinline__ void vl_gemm(const CUtensorMap& tmA, const CUtensorMa
       vl_commit<PAIR>(drain);
     }
   } else {
-    // ------------------------------- epilogue: one row per thread -------------------------------
-    const int q = warp & 3;
+    // ------------------ epilogue: one row and one half of the tile's columns per thread ------------------
+    const int q = warp & 3, side = (warp - 2) >> 2, hn = p.bn / 2;
+    const uint32_t out_buf = smem_u32(sE + (warp - 2) * kVlStore);
     const int tn = p.bn;
     int lt = 0;
     for (int i = worker; i < num_items; i += workers, ++lt) {
       const Item t = item(i);
       const int b = lt & 1, u = lt >> 1;
+      const int in_tile = rank * kVlM + 32 * q + lane, row = t.m0 + in_tile;
+      const bool live = row < rows;
+      const int ncol = min(tn, p.cols - t.n0);
+      float ly = 0.0f;
+      int yt = -1;
+      if (!GRAD && live) {             // on their way while the tile is computed
+        ly = p.ly[row];
+        yt = p.target[row] - t.n0;
+      }
       const bool ok = mbar_wait(&tfull[b], u & 1);
       if (!__all_sync(0xffffffffu, ok && !*abort_flag)) { *abort_flag = 1; break; }
       tc_fence_after();
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(b * kVlN);
-      const int in_tile = rank * kVlM + 32 * q + lane, row = t.m0 + in_tile;
-      const bool live = row < rows;
-      const int ncol = min(tn, p.cols - t.n0);
+      auto release = [&]() {           // the accumulator has been read
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (PAIR)
+            asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(vl_peer(smem_u32(&tempty[b]), 0))
+                         : "memory");
+          else
+            mbar_arrive(&tempty[b]);
+        }
+      };
       if constexpr (!GRAD) {
-        const float ly = live ? p.ly[row] : 0.0f;
-        const int yt = live ? p.target[row] - t.n0 : -1;
         const int y = (yt >= 0 && yt < ncol) ? yt : -1;          // the target's column, if it is here
-        // the largest d (the target's own column is left out); a NaN shows in the sum below
-        float top = -INFINITY;
+        // One pass against the target's logit, the target's own column left out; a second one, relative to the
+        // half tile's largest d, only for the rare warp with a row whose weights could overflow. A NaN shows in the
+        // sum. Chunks of 32 columns that are whole and hold no target of the warp's rows need no checks.
+        const int c_end = min(ncol, (side + 1) * hn);
+        float top = -INFINITY, shift = 0.0f, sum = 0.0f;
+        while (true) {
+          const float ref = ly + shift;
+          float part[4] = {}, high[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-        for (int c = 0; c < ncol; c += 16) {
-          uint32_t v[16];
-          tmem_ld16(taddr + c, v);
-          tmem_wait_ld();
+          for (int c = side * hn; c < c_end; c += 32) {
+            uint32_t v[2][16];
+            tmem_ld16(taddr + c, v[0]);
+            tmem_ld16(taddr + c + 16, v[1]);
+            const bool check = c + 32 > c_end || __any_sync(0xffffffffu, y >= c && y < c + 32);
+            tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float l = __uint_as_float(v[j]);
-            if (c + j < ncol && c + j != y) top = fmaxf(top, l);
+            for (int h = 0; h < 2; ++h) {
+              if (c + 16 * h >= c_end) break;
+              float e[16];
+              if (check) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                  const float l = __uint_as_float(v[h][j]);
+                  const bool other = c + 16 * h + j < c_end && c + 16 * h + j != y;
+                  if (other) high[j & 3] = fmaxf(high[j & 3], l);
+                  e[j] = other ? __expf(l - ref) : 0.0f;
+                }
+              } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                  const float l = __uint_as_float(v[h][j]);
+                  high[j & 3] = fmaxf(high[j & 3], l);
+                  e[j] = __expf(l - ref);
+                }
+              }
+#pragma unroll
+              for (int j = 0; j < 16; ++j) part[j & 3] += e[j];
+              if (p.weights) {
+                uint32_t o[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] = pack_bf16x2(e[2 * j], e[2 * j + 1]);
+                // 64-byte rows, 16-byte piece k of row r at k ^ (r / 2 % 4): no bank conflicts either way
+                const uint32_t at = out_buf + 64u * lane, x = (lane >> 1) & 3;
+                st_shared_v4(at + (((2 * h) ^ x) << 4), o[0], o[1], o[2], o[3]);
+                st_shared_v4(at + (((2 * h + 1) ^ x) << 4), o[4], o[5], o[6], o[7]);
+              }
+            }
+            if (p.weights) {                     // out in whole 64-byte runs of 8 rows at a time
+              __syncwarp();
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int r = 8 * k + (lane >> 2), pc = lane & 3;
+                uint4 o;
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w)
+                             : "r"(out_buf + 64u * r + ((pc ^ ((r >> 1) & 3)) << 4)) : "memory");
+                const int wr = row - lane + r;   // the pitch has room up to a multiple of 16 words
+                if (wr < rows && c + 8 * pc < c_end)
+                  *reinterpret_cast<uint4*>(p.weights + wr * p.pitch + t.n0 + c + 8 * pc) = o;
+              }
+            }
+            __syncwarp();                        // the next tcgen05.ld is warp-wide
           }
+          top = fmaxf(fmaxf(high[0], high[1]), fmaxf(high[2], high[3]));
+          sum = (part[0] + part[1]) + (part[2] + part[3]);
+          const bool far = shift == 0.0f && top - ly > kVlMaxShift;
+          if (far) shift = top - ly;
+          if (!__any_sync(0xffffffffu, far)) break;
         }
-        const float shift = top - ly > kVlMaxShift ? top - ly : 0.0f;
-        const float ref = ly + shift;
-        float sum = 0.0f;
-#pragma unroll 1
-        for (int c = 0; c < ncol; c += 16) {
-          uint32_t v[16];
-          tmem_ld16(taddr + c, v);
-          tmem_wait_ld();
-          uint32_t o[8];
-          float e[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float w = __expf(__uint_as_float(v[j]) - ref);
-            e[j] = (c + j < ncol && c + j != y) ? w : 0.0f;
-          }
-          float part = 0.0f;
-#pragma unroll
-          for (int j = 0; j < 16; ++j) part += e[j];
-          sum += part;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] = pack_bf16x2(e[2 * j], e[2 * j + 1]);
-          if (p.weights && live) {               // the pitch has room up to a multiple of 16 words
-            uint4* dst = reinterpret_cast<uint4*>(p.weights + row * p.pitch + t.n0 + c);
-            dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-            dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
-          }
-          __syncwarp();                          // the next tcgen05.ld is warp-wide
-        }
-        if (live) p.stats[static_cast<int64_t>(t.n0 / tn) * p.rows_max + row] = make_float2(shift, sum);
+        release();                     // before the store below, which the arrival would wait for
+        if (live) p.stats[static_cast<int64_t>(2 * (t.n0 / tn) + side) * p.rows_max + row] = make_float2(shift, sum);
       } else {
         const bool whole = i < deal.full || deal.cuts == 1;
         const float f = whole && live ? p.factor[row] : 0.0f;
         __nv_bfloat16* out = p.out + static_cast<int64_t>(whole && live ? p.token[row] : 0) * p.cols + t.n0;
         float* part = whole ? nullptr : p.part + (static_cast<int64_t>(i - deal.full) * kVlM * C::CTAS + in_tile) * kVlN;
+        const int c_end = min(ncol, (side + 1) * hn);
 #pragma unroll 1
-        for (int c = 0; c < ncol; c += 16) {
+        for (int c = side * hn; c < c_end; c += 16) {
           uint32_t v[16];
           tmem_ld16(taddr + c, v);
           tmem_wait_ld();
 #pragma unroll
           for (int h = 0; h < 2; ++h) {          // K % 8 == 0: whole groups of 8
-            if (!live || c + 8 * h >= ncol) break;
+            if (!live || c + 8 * h >= c_end) break;
             if (whole) {
               uint32_t o[4];
 #pragma unroll
@@ -349,15 +412,7 @@ __device__ __forceinline__ void vl_gemm(const CUtensorMap& tmA, const CUtensorMa
           }
           __syncwarp();
         }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if constexpr (PAIR)
-          asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(vl_peer(smem_u32(&tempty[b]), 0))
-                       : "memory");
-        else
-          mbar_arrive(&tempty[b]);
+        release();
       }
     }
   }
@@ -384,74 +439,94 @@ __device__ __forceinline__ void vl_gemm(const CUtensorMap& tmA, const CUtensorMa
 template <bool GRAD>
 __global__ void __launch_bounds__(kVlThreads, 1)
     vl_gemm1_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA2,
-                    const __grid_constant__ CUtensorMap tmB, const __grid_constant__ VlParams p) {
+                    const __grid_constant__ CUtensorMap tmB,
+                    const __grid_constant__ VlParams p) {
   vl_gemm<GRAD, false>(tmA, tmA2, tmB, p);
 }
 template <bool GRAD>
 __global__ void __launch_bounds__(kVlThreads, 1) __cluster_dims__(2, 1, 1)
     vl_gemm2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA2,
-                    const __grid_constant__ CUtensorMap tmB, const __grid_constant__ VlParams p) {
+                    const __grid_constant__ CUtensorMap tmB,
+                    const __grid_constant__ VlParams p) {
   vl_gemm<GRAD, true>(tmA, tmA2, tmB, p);
 }
 
-// Numbers the tokens in the loss: one CTA, tokens in order. A token left out (ignored, or with a target outside
-// the vocabulary, which the status word reports) has a loss of 0.
+// Numbers the tokens in the loss, in order: one CTA, 8192 tokens at a time. token[i] is the i-th of them, target[i]
+// its target; the tokens left out (ignored, or with a target outside the vocabulary, which the status word
+// reports) fill `token` from its end and have a loss of 0.
 template <typename TI>
 __global__ void __launch_bounds__(1024) vl_index_kernel(const TI* __restrict__ targets, int T, int64_t V, int64_t ignore,
                                                         int* __restrict__ token, int* __restrict__ target,
                                                         float* __restrict__ loss, int* __restrict__ count) {
-  __shared__ int sm[32];
-  __shared__ int base;
+  constexpr int PER = 8;
+  __shared__ int sm[PER][32], all[PER];      // per 1024 tokens: each warp's count, then what lies before it; the sum
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) base = 0;
-  for (int t0 = 0; t0 < T; t0 += blockDim.x) {
-    const int t = t0 + threadIdx.x;
-    const int64_t y = t < T ? static_cast<int64_t>(targets[t]) : ignore;
-    const bool in = t < T && y != ignore && y >= 0 && y < V;
-    if (t < T && !in) {
-      if (y != ignore) raise_status(kStatusTarget);
-      loss[t] = 0.0f;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  int base = 0;
+  for (int64_t t0 = 0; t0 < T; t0 += PER * 1024) {
+    int64_t y[PER];
+    unsigned votes[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int64_t t = t0 + 1024 * k + threadIdx.x;
+      y[k] = t < T ? static_cast<int64_t>(targets[t]) : ignore;
     }
-    const unsigned votes = __ballot_sync(0xffffffffu, in);
-    if (lane == 0) sm[warp] = __popc(votes);
-    __syncthreads();
-    int before = base + __popc(votes & ((1u << lane) - 1u));
-    for (int w = 0; w < warp; ++w) before += sm[w];
-    if (in) {
-      token[before] = t;
-      target[before] = static_cast<int>(y);
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      votes[k] = __ballot_sync(0xffffffffu, y[k] != ignore && y[k] >= 0 && y[k] < V);
+      if (lane == 0) sm[k][warp] = __popc(votes[k]);
     }
     __syncthreads();
-    if (threadIdx.x == blockDim.x - 1) base = before + (in ? 1 : 0);
+    if (warp < PER) {
+      const int mine = sm[warp][lane];
+      int upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+      }
+      sm[warp][lane] = upto - mine;
+      if (lane == 31) all[warp] = upto;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int64_t t = t0 + 1024 * k + threadIdx.x;
+      const int before = base + sm[k][warp] + __popc(votes[k] & ((1u << lane) - 1u));
+      if (votes[k] >> lane & 1u) {
+        token[before] = static_cast<int>(t);
+        target[before] = static_cast<int>(y[k]);
+      } else if (t < T) {
+        if (y[k] != ignore) raise_status(kStatusTarget);
+        token[T - 1 - (t - before)] = static_cast<int>(t);
+        loss[t] = 0.0f;
+      }
+      base += all[k];
+    }
     __syncthreads();
   }
   if (threadIdx.x == 0) *count = base;
 }
 
-// One warp per row of the piece: the target's logit in fp32, and the row's place in the packed copy where tokens
-// are left out (packed: T, or 0 for no copy). Behind them, with dX, one warp per token of the whole call that
-// zeroes the gradient of a token left out (found by its number: tokens in the loss are in order).
-__global__ void __launch_bounds__(256) vl_target_kernel(const __nv_bfloat16* __restrict__ X,
-                                                        const __nv_bfloat16* __restrict__ W, int K, int r0, int rows_max,
-                                                        int T, const int* __restrict__ count,
-                                                        const int* __restrict__ token, const int* __restrict__ target,
-                                                        float* __restrict__ ly, __nv_bfloat16* __restrict__ packed,
-                                                        __nv_bfloat16* __restrict__ dX) {
-  const int lane = threadIdx.x & 31;
-  const int i = static_cast<int>(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32;
+// Four warps per row of the piece: the target's logit in fp32, and the row's place in the packed copy where tokens
+// are left out. Behind them, with dX, four warps per token left out of the whole call, which zero its gradient.
+constexpr int kVlRowThreads = 128;
+__global__ void __launch_bounds__(kVlRowThreads) vl_target_kernel(const __nv_bfloat16* __restrict__ X,
+                                                                  const __nv_bfloat16* __restrict__ W, int K, int r0,
+                                                                  int rows_max, int T, const int* __restrict__ count,
+                                                                  const int* __restrict__ token,
+                                                                  const int* __restrict__ target, float* __restrict__ ly,
+                                                                  __nv_bfloat16* __restrict__ packed,
+                                                                  __nv_bfloat16* __restrict__ dX) {
+  __shared__ float sm[kVlRowThreads / 32];
+  vl_chain();
+  const int lane = threadIdx.x & 31, i = blockIdx.x;
   const int n = *count;
   if (i >= rows_max) {
-    const int t = i - rows_max;
-    if (!dX || t >= T || n == T) return;
-    int lo = 0, hi = n;                  // the first number whose token is not before t
-    while (lo < hi) {
-      const int mid = (lo + hi) / 2;
-      if (token[mid] < t) lo = mid + 1;
-      else hi = mid;
-    }
-    if (lo < n && token[lo] == t) return;
+    if (!dX || n + (i - rows_max) >= T) return;
+    const int t = token[n + (i - rows_max)];
     uint4* d = reinterpret_cast<uint4*>(dX + static_cast<int64_t>(t) * K);
-    for (int c = lane; c < K / 8; c += 32) d[c] = make_uint4(0, 0, 0, 0);
+    for (int c = threadIdx.x; c < K / 8; c += kVlRowThreads) d[c] = make_uint4(0, 0, 0, 0);
     return;
   }
   if (i >= vl_rows(count, r0, rows_max)) return;
@@ -459,8 +534,8 @@ __global__ void __launch_bounds__(256) vl_target_kernel(const __nv_bfloat16* __r
   const uint4* w = reinterpret_cast<const uint4*>(W + static_cast<int64_t>(target[r0 + i]) * K);
   uint4* to = n < T ? reinterpret_cast<uint4*>(packed + static_cast<int64_t>(i) * K) : nullptr;
   float acc = 0.0f;
-#pragma unroll 4
-  for (int c = lane; c < K / 8; c += 32) {
+#pragma unroll 8
+  for (int c = threadIdx.x; c < K / 8; c += kVlRowThreads) {
     const uint4 a = x[c], b = w[c];
     if (to) to[c] = a;
     const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
@@ -474,53 +549,84 @@ __global__ void __launch_bounds__(256) vl_target_kernel(const __nv_bfloat16* __r
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-  if (lane == 0) ly[i] = acc;
+  if (lane == 0) sm[threadIdx.x >> 5] = acc;
+  __syncthreads();
+  if (threadIdx.x == 0) ly[i] = (sm[0] + sm[1]) + (sm[2] + sm[3]);
 }
 
-// One warp per row of the piece. bn: words per tile of the logits.
-__global__ void __launch_bounds__(256) vl_finish_kernel(const float2* __restrict__ stats, int r0, int rows_max, int tiles,
+// 32 rows per CTA: lanes are rows (the statistics of 32 rows of a tile are one run of memory), warps share the tiles;
+// their sums are added in warp order. tiles, bn: half tiles of the logits and their words.
+constexpr int kVlFinishThreads = 1024;
+__global__ void __launch_bounds__(kVlFinishThreads) vl_finish_kernel(const float2* __restrict__ stats, int r0, int rows_max, int tiles,
                                                         int bn, const int* __restrict__ count, const int* __restrict__ token,
                                                         const int* __restrict__ target, int V,
                                                         const float* __restrict__ dloss, int mean, float* __restrict__ loss,
                                                         __nv_bfloat16* weights, int64_t pitch, float* __restrict__ factor) {
-  const int lane = threadIdx.x & 31;
-  const int row = static_cast<int>(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32;
-  if (row >= vl_rows(count, r0, rows_max)) return;
-  float shift = 0.0f;                 // the row's: the largest of its tiles'
-  for (int i = lane; i < tiles; i += 32) shift = fmaxf(shift, stats[static_cast<int64_t>(i) * rows_max + row].x);
+  constexpr int W = kVlFinishThreads / 32;
+  __shared__ float2 sm[W][32];
+  __shared__ float row_shift[32];
+  vl_chain();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = static_cast<int>(blockIdx.x) * 32 + lane, rows = vl_rows(count, r0, rows_max);
+  const bool live = row < rows;
+  // (shift, sum relative to exp(shift)) of this warp's tiles
+  auto add = [](float2& a, float2 b) {
+    if (b.x > a.x) {
+      a.y = a.y * expf(a.x - b.x) + b.y;
+      a.x = b.x;
+    } else {
+      a.y += b.x < a.x ? b.y * expf(b.x - a.x) : b.y;
+    }
+  };
+  float2 a = make_float2(0.0f, 0.0f);
+  if (live) {
+    for (int i = warp; i < tiles; i += 8 * W) {
+      float2 b[8];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) shift = fmaxf(shift, __shfl_xor_sync(0xffffffffu, shift, o));
-  float z = 0.0f;
-  for (int i = lane; i < tiles; i += 32) {
-    const float2 s = stats[static_cast<int64_t>(i) * rows_max + row];
-    z += shift > 0.0f ? s.y * expf(s.x - shift) : s.y;
+      for (int k = 0; k < 8; ++k)
+        b[k] = i + k * W < tiles ? stats[static_cast<int64_t>(i + k * W) * rows_max + row] : make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) add(a, b[k]);
+    }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-  const float one = shift > 0.0f ? expf(-shift) : 1.0f;
-  const int t = token[r0 + row];
-  if (lane == 0) loss[t] = shift > 0.0f ? shift + logf(z + one) : log1pf(z);
+  sm[warp][lane] = a;
+  __syncthreads();
+  if (warp == 0) {
+    for (int w = 1; w < W; ++w) add(a, sm[w][lane]);
+    row_shift[lane] = a.x;
+    if (live) {
+      const float one = a.x > 0.0f ? expf(-a.x) : 1.0f;
+      const int t = token[r0 + row];
+      loss[t] = a.x > 0.0f ? a.x + logf(a.y + one) : log1pf(a.y);
+      if (weights) {
+        float g = dloss ? dloss[t] : 1.0f;
+        if (mean) g /= static_cast<float>(*count);
+        factor[row] = g / (a.y + one);
+      }
+    }
+  }
   if (!weights) return;
-  __nv_bfloat16* w = weights + static_cast<int64_t>(row) * pitch;
-  if (shift > 0.0f) {
-    for (int v = lane; v < V; v += 32) {
-      const float s = stats[static_cast<int64_t>(v / bn) * rows_max + row].x;
+  __syncthreads();
+  // rows with shifts: every weight relative to the row's (rare: a target 40 below another word)
+  for (int i = 0; i < 32; ++i) {
+    const float shift = row_shift[i];
+    const int r = static_cast<int>(blockIdx.x) * 32 + i;
+    if (!(shift > 0.0f) || r >= rows) continue;
+    __nv_bfloat16* w = weights + static_cast<int64_t>(r) * pitch;
+    for (int v = threadIdx.x; v < V; v += blockDim.x) {
+      const float s = stats[static_cast<int64_t>(v / bn) * rows_max + r].x;
       if (s != shift) w[v] = __float2bfloat16_rn(__bfloat162float(w[v]) * expf(s - shift));
     }
-    __syncwarp();
   }
-  if (lane == 0) {
-    w[target[r0 + row]] = __float2bfloat16_rn(-z);
-    float g = dloss ? dloss[t] : 1.0f;
-    if (mean) g /= static_cast<float>(*count);
-    factor[row] = g / (z + one);
-  }
+  __syncthreads();
+  if (warp == 0 && live) weights[static_cast<int64_t>(row) * pitch + target[r0 + row]] = __float2bfloat16_rn(-a.y);
 }
 
-// The tiles of dX that were cut: their partial sums in order. One CTA per tile and 16 of its rows.
+// The tiles of dX that were cut: their partial sums in order. One CTA per tile and 8 of its rows.
 template <int CTAS>
 __global__ void __launch_bounds__(256) vl_reduce_kernel(const __grid_constant__ VlParams p, int workers) {
   constexpr int MT = kVlM * CTAS;
+  vl_chain();
   const int rows = vl_rows(p.count, p.r0, p.rows_max);
   const int tiles_m = (rows + MT - 1) / MT;
   const VlDeal deal = vl_deal(tiles_m * p.tiles_n, workers, p.nkb);
@@ -528,25 +634,23 @@ __global__ void __launch_bounds__(256) vl_reduce_kernel(const __grid_constant__ 
   if (deal.cuts == 1 || r >= deal.rest) return;
   const int m0 = tile % tiles_m * MT, n0 = tile / tiles_m * p.bn;
   const int ncol = min(p.bn, p.cols - n0);
-  for (int e = threadIdx.x; e < 16 * (kVlN / 8); e += blockDim.x) {
-    const int in_tile = blockIdx.y * 16 + e / (kVlN / 8), row = m0 + in_tile, c = e % (kVlN / 8) * 8;
-    if (row >= rows || c >= ncol) continue;
-    float acc[8] = {};
-#pragma unroll 4
-    for (int w = 0; w < deal.cuts; ++w) {
-      const float4* src = reinterpret_cast<const float4*>(
-          p.part + (static_cast<int64_t>(w * deal.rest + r) * MT + in_tile) * kVlN + c);
-      const float4 a = src[0], b = src[1];
-      acc[0] += a.x; acc[1] += a.y; acc[2] += a.z; acc[3] += a.w;
-      acc[4] += b.x; acc[5] += b.y; acc[6] += b.z; acc[7] += b.w;
-    }
-    const float f = p.factor[row];
-    uint4 o = make_uint4(0, 0, 0, 0);
-    if (f != 0.0f)
-      o = make_uint4(pack_bf16x2(acc[0] * f, acc[1] * f), pack_bf16x2(acc[2] * f, acc[3] * f),
-                     pack_bf16x2(acc[4] * f, acc[5] * f), pack_bf16x2(acc[6] * f, acc[7] * f));
-    *reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(p.token[row]) * p.cols + n0 + c) = o;
+  const int in_tile = blockIdx.y * 8 + threadIdx.x / (kVlN / 8), row = m0 + in_tile, c = threadIdx.x % (kVlN / 8) * 8;
+  if (row >= rows || c >= ncol) return;
+  float acc[8] = {};
+#pragma unroll 8
+  for (int w = 0; w < deal.cuts; ++w) {
+    const float4* src = reinterpret_cast<const float4*>(
+        p.part + (static_cast<int64_t>(w * deal.rest + r) * MT + in_tile) * kVlN + c);
+    const float4 a = src[0], b = src[1];
+    acc[0] += a.x; acc[1] += a.y; acc[2] += a.z; acc[3] += a.w;
+    acc[4] += b.x; acc[5] += b.y; acc[6] += b.z; acc[7] += b.w;
   }
+  const float f = p.factor[row];
+  uint4 o = make_uint4(0, 0, 0, 0);
+  if (f != 0.0f)
+    o = make_uint4(pack_bf16x2(acc[0] * f, acc[1] * f), pack_bf16x2(acc[2] * f, acc[3] * f),
+                   pack_bf16x2(acc[4] * f, acc[5] * f), pack_bf16x2(acc[6] * f, acc[7] * f));
+  *reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(p.token[row]) * p.cols + n0 + c) = o;
 }
 
 // total = sum of the tokens' losses (fp64, fixed order), over their count for a mean (0 / 0 = NaN when no
@@ -554,6 +658,7 @@ __global__ void __launch_bounds__(256) vl_reduce_kernel(const __grid_constant__ 
 __global__ void __launch_bounds__(1024) vl_total_kernel(const float* __restrict__ loss, int64_t T, int mean,
                                                         const int* __restrict__ count, float* __restrict__ total) {
   __shared__ double sm[32];
+  vl_chain();
   double a = 0.0;
   for (int64_t i = threadIdx.x; i < T; i += blockDim.x) a += loss[i];
 #pragma unroll

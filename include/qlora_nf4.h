@@ -357,8 +357,8 @@ int qlora_rope(const qlora_rope_tensor* x, int nx, int dtype, int64_t B, int64_t
  * A target that is neither ignore_index nor in [0, V) sets QLORA_STATUS_TARGET; its token is then treated
  * as ignored. fp32 logits and sums; the softmax weights are rounded to bf16 for the gradient's product.
  * Rules: T, V >= 1 (V < 2^30), K % 8 == 0, 8 <= K <= 2^20. `workspace` >= qlora_vocab_loss_workspace(T, V, K,
- * dX != NULL), at most about 128 MB for the weights of one piece of the tokens plus 2 K/V of that for the
- * partial sums of short inputs and 16 bytes per token. Deterministic.
+ * dX != NULL): with dX about 128 MB for the weights of one piece of the tokens (two bytes per token and word of
+ * it) and 58 MB of partial sums, a copy of the piece's rows of X, and 12 bytes per token. Deterministic.
  */
 enum { QLORA_LOSS_NONE = 0, QLORA_LOSS_SUM = 1, QLORA_LOSS_MEAN = 2 };
 int qlora_vocab_loss_workspace(int64_t T, int64_t V, int64_t K, int gradient, size_t* bytes);
