@@ -878,22 +878,24 @@ int launch_codebook_linear4(ClParams p, const CodebookArg& cb, int sms, cudaStre
 constexpr double kTwoPi = 6.283185307179586476925286766559;
 
 template <typename T, int VE, int AL, bool HALF>
-int launch_rope(RopeParams& p, bool copy_tail, int sms, cudaStream_t st) {
+int launch_rope(RopeParams& p, bool copy_tail, int64_t step, int sms, cudaStream_t st) {
+  constexpr int W = 16 / sizeof(T);
   p.units = HALF ? p.rotary_dim / (2 * VE) : p.rotary_dim / VE;
-  p.tail = copy_tail ? static_cast<int>(cdiv(p.head_dim - p.rotary_dim, VE)) : 0;
+  p.tail = copy_tail ? static_cast<int>(cdiv(p.head_dim - p.rotary_dim, W)) : 0;
+  p.tail_aligned = step % W == 0 && p.rotary_dim % W == 0 ? 1 : 0;
   const int per_head = p.units + p.tail;
+  const int64_t gz = std::min<int64_t>(p.B, 65535);
   p.slots = std::max(1, std::min(kRopeThreads / per_head, p.heads));
-  // four tokens share a CTA's set-up once that still leaves every SM several CTAs; heads are split over CTAs
-  // where there are few tokens
-  const int tok = p.tokens >= int64_t(sms) * 16 ? 4 : 1;
-  const int64_t gx = cdiv(p.tokens, tok);
-  const int64_t want = cdiv(int64_t(sms) * 4, gx), most = cdiv(p.heads, p.slots);
-  const int64_t gy = std::max<int64_t>(1, std::min(want, most));
-  p.heads_per_cta = static_cast<int>(cdiv(cdiv(p.heads, gy), p.slots) * p.slots);
-  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(cdiv(p.heads, p.heads_per_cta)));
   const unsigned threads = static_cast<unsigned>(per_head * p.slots);
+  // two tokens share a CTA's set-up once that still leaves every SM several CTAs; where there are few tokens their
+  // heads are split over CTAs
+  const int tok = p.B * p.T >= int64_t(sms) * 16 ? kRopeTokens : 1;
+  const int64_t gx = cdiv(p.T, tok), most = cdiv(p.heads, p.slots);
+  const int64_t gy = std::max<int64_t>(1, std::min(cdiv(int64_t(sms) * 4, gx * gz), most));
+  p.heads_per_cta = static_cast<int>(cdiv(cdiv(p.heads, gy), p.slots) * p.slots);
+  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(cdiv(p.heads, p.heads_per_cta)), static_cast<unsigned>(gz));
   const size_t smem = static_cast<size_t>(tok) * p.rotary_dim * 4;
-  if (tok == 4) rope_kernel<T, VE, AL, HALF, 4><<<grid, threads, smem, st>>>(p);
+  if (tok > 1) rope_kernel<T, VE, AL, HALF, kRopeTokens><<<grid, threads, smem, st>>>(p);
   else rope_kernel<T, VE, AL, HALF, 1><<<grid, threads, smem, st>>>(p);
   return launched();
 }
@@ -904,15 +906,15 @@ int launch_rope_type(RopeParams& p, bool half, bool copy_tail, int64_t step, int
   const int64_t pairs = half ? p.rotary_dim / 2 : p.rotary_dim;
   auto fits = [&](int ve) { return pairs % ve == 0 && step % ve == 0; };
   if (half) {
-    if (W == 8 && fits(8)) return launch_rope<T, W, W, true>(p, copy_tail, sms, st);
-    if (fits(4)) return launch_rope<T, 4, 4, true>(p, copy_tail, sms, st);
-    if (fits(2)) return launch_rope<T, 2, 2, true>(p, copy_tail, sms, st);
-    return launch_rope<T, 1, 1, true>(p, copy_tail, sms, st);
+    if (W == 8 && fits(8)) return launch_rope<T, W, W, true>(p, copy_tail, step, sms, st);
+    if (fits(4)) return launch_rope<T, 4, 4, true>(p, copy_tail, step, sms, st);
+    if (fits(2)) return launch_rope<T, 2, 2, true>(p, copy_tail, step, sms, st);
+    return launch_rope<T, 1, 1, true>(p, copy_tail, step, sms, st);
   }
-  if (W == 8 && fits(8)) return launch_rope<T, W, W, false>(p, copy_tail, sms, st);
-  if (fits(4)) return launch_rope<T, 4, 4, false>(p, copy_tail, sms, st);
-  if (fits(2)) return launch_rope<T, 2, 2, false>(p, copy_tail, sms, st);
-  return launch_rope<T, 2, 1, false>(p, copy_tail, sms, st);
+  if (W == 8 && fits(8)) return launch_rope<T, W, W, false>(p, copy_tail, step, sms, st);
+  if (fits(4)) return launch_rope<T, 4, 4, false>(p, copy_tail, step, sms, st);
+  if (fits(2)) return launch_rope<T, 2, 2, false>(p, copy_tail, step, sms, st);
+  return launch_rope<T, 2, 1, false>(p, copy_tail, step, sms, st);
 }
 
 // ---- vocabulary loss -------------------------------------------------------------------------------
@@ -1506,8 +1508,8 @@ int qlora_rope(const qlora_rope_tensor* x, int nx, int dtype, int64_t B, int64_t
   if (int e = check_device(&sms)) return e;
   p.heads0 = static_cast<int>(x[0].heads);
   p.heads = static_cast<int>(heads);
+  p.B = B;
   p.T = T;
-  p.tokens = B * T;
   p.rotary_dim = rotary_dim;
   p.head_dim = head_dim;
   p.positions = positions;
