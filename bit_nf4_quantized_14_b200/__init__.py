@@ -24,6 +24,7 @@ import contextlib
 import ctypes
 import functools
 import os
+import struct
 from dataclasses import dataclass
 
 import numpy as np
@@ -98,7 +99,7 @@ def _open() -> ctypes.CDLL:
         "qlora_codebook_linear": [vp, i64, vp, vp, i64, i64, P(ctypes.c_float), i32, vp, vp],
         "qlora_rope_frequencies": [i32, ctypes.c_double, i32, ctypes.c_double, ctypes.c_double, ctypes.c_double,
                                    ctypes.c_double, P(ctypes.c_double), P(ctypes.c_double)],
-        "qlora_rope": [P(_RopeTensor), i32, i32, i64, i64, i32, i32, i32, P(ctypes.c_double), ctypes.c_double, vp, i32,
+        "qlora_rope": [vp, i32, i32, i64, i64, i32, i32, i32, P(ctypes.c_double), ctypes.c_double, vp, i32,
                        i64, i64, i32, vp],
         "qlora_vocab_loss_workspace": [i64, i64, i64, i32, P(sz)],
         "qlora_vocab_loss": [vp, i64, vp, i64, i64, vp, i32, i64, i32, vp, vp, vp, vp, vp, sz, vp],
@@ -146,15 +147,15 @@ def _need(t: torch.Tensor, dtype, name: str) -> None:
 _HERE_ALREADY = contextlib.nullcontext()
 
 
-def _on(device: torch.device):
+def _on(device: int):
     """The device made current for a call whose tensors live there."""
-    return _HERE_ALREADY if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
+    return _HERE_ALREADY if device == torch._C._cuda_getDevice() else torch.cuda.device(device)
 
 
-def _same_device(device, **tensors) -> None:
+def _same_device(device: int, **tensors) -> None:
     for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"{name}: expected a tensor on cuda:{device}, got {t.device}")
 
 
 # ---- host-only queries --------------------------------------------------------------------------
@@ -385,16 +386,19 @@ def codebook_linear(X: torch.Tensor, codes: torch.Tensor, absmax: torch.Tensor, 
     T, K = X.shape
     if codes.numel() != -(-N * K // 2) or absmax.numel() != -(-N * K // 64):
         raise ValueError(f"codebook_linear: codes / absmax are not those of a {N} x {K} weight")
-    Y = out if out is not None else torch.empty(T, N, dtype=torch.bfloat16, device=X.device)
-    _need(Y, torch.bfloat16, "out")
-    if Y.numel() != T * N:
-        raise ValueError(f"codebook_linear: out must be {T} x {N}")
-    _same_device(X.device, codes=codes, absmax=absmax, out=Y)
+    if out is None:
+        out = torch.empty((T, N), dtype=torch.bfloat16, device=X.device)
+    else:
+        _need(out, torch.bfloat16, "out")
+        if out.numel() != T * N:
+            raise ValueError(f"codebook_linear: out must be {T} x {N}")
+    dev = X.get_device()
+    _same_device(dev, codes=codes, absmax=absmax, out=out)
     lv, nl = _level_array(tuple(levels))
-    with _on(X.device):
-        _check(load().qlora_codebook_linear(_ptr(X), T, _ptr(codes), _ptr(absmax), N, K, lv, nl, _ptr(Y),
-                                            _stream(stream)), "qlora_codebook_linear")
-    return Y
+    with _on(dev):
+        _check(load().qlora_codebook_linear(X.data_ptr(), T, codes.data_ptr(), absmax.data_ptr(), N, K, lv, nl,
+                                            out.data_ptr(), _stream(stream)), "qlora_codebook_linear")
+    return out
 
 
 def linear_single(X: torch.Tensor, q: NF4SingleWeight, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -445,11 +449,18 @@ def _rope_setup(c: RotaryConfig):
     return th, m.value if c.mscale is None else float(c.mscale), ROPE_LAYOUTS[c.layout]
 
 
-def _rope_side(x: torch.Tensor, o: torch.Tensor) -> tuple:
-    xs, os_ = x.stride(), o.stride()
-    if x.dim() == 3:
-        return x.data_ptr(), o.data_ptr(), x.shape[1], 0, xs[0], xs[1], 0, os_[0], os_[1]
-    return x.data_ptr(), o.data_ptr(), x.shape[2], xs[0], xs[1], xs[2], os_[0], os_[1], os_[2]
+_ROPE_SIDE = struct.Struct("9q")        # qlora_rope_tensor
+_ROPE_TYPES = {torch.float32: QLORA_F32, torch.bfloat16: QLORA_BF16}
+
+
+def _rope_side(x: torch.Tensor, o: torch.Tensor) -> bytes:
+    xs = x.stride()
+    os_ = o.stride()
+    if xs[-1] != 1 or os_[-1] != 1:
+        raise ValueError("rotary: the features of a head must be contiguous")
+    if len(xs) == 3:
+        return _ROPE_SIDE.pack(x.data_ptr(), o.data_ptr(), x.shape[1], 0, xs[0], xs[1], 0, os_[0], os_[1])
+    return _ROPE_SIDE.pack(x.data_ptr(), o.data_ptr(), x.shape[2], *xs[:3], *os_[:3])
 
 
 def rotary(q: torch.Tensor, k: torch.Tensor | None, config: RotaryConfig, positions: torch.Tensor | None = None,
@@ -459,36 +470,41 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, config: RotaryConfig, positi
     int32 or int64, (T,) or (B, T), plus `offset`; without positions token t sits at offset + t. inverse turns
     back, which is the gradient. out: a pair of tensors like (q, k), the inputs themselves for in place.
     Returns (q', k')."""
-    if q.dim() not in (3, 4) or q.dtype not in (torch.float32, torch.bfloat16) or not q.is_cuda:
+    shape = q.shape
+    dtype = _ROPE_TYPES.get(q.dtype)
+    if len(shape) not in (3, 4) or dtype is None or not q.is_cuda:
         raise ValueError("rotary: q must be a (T, heads, dim) or (B, T, heads, dim) CUDA tensor of float32 or bfloat16")
-    lead = q.shape[:-2]
-    if k is not None and (k.dtype != q.dtype or k.shape[:-2] != lead or k.shape[-1] != q.shape[-1]):
-        raise ValueError("rotary: k must match q in type, tokens and head size")
+    dev = q.get_device()
     qo, ko = (None, None) if out is None else out
     qo = torch.empty_like(q) if qo is None else qo
-    ko = (torch.empty_like(k) if ko is None else ko) if k is not None else None
-    _same_device(q.device, k=k, out=qo, k_out=ko, positions=positions)
-    for x, o in ((q, qo), (k, ko)):
-        if x is not None and (o.shape != x.shape or o.dtype != x.dtype):
+    if qo.shape != shape or qo.dtype != q.dtype:
+        raise ValueError("rotary: out must match the inputs")
+    sides = _rope_side(q, qo)
+    if k is not None:
+        if k.dtype != q.dtype or k.shape[:-2] != shape[:-2] or k.shape[-1] != shape[-1]:
+            raise ValueError("rotary: k must match q in type, tokens and head size")
+        ko = torch.empty_like(k) if ko is None else ko
+        if ko.shape != k.shape or ko.dtype != k.dtype:
             raise ValueError("rotary: out must match the inputs")
-        if x is not None and (x.stride(-1) != 1 or o.stride(-1) != 1):
-            raise ValueError("rotary: the features of a head must be contiguous")
+        sides += _rope_side(k, ko)
+    else:
+        ko = None
+    _same_device(dev, k=k, out=qo, k_out=ko, positions=positions)
     th, mscale, layout = _rope_setup(config)
-    B, T = lead if len(lead) == 2 else (1, lead[0])
-    pos_b = 0
+    B, T = shape[:2] if len(shape) == 4 else (1, shape[0])
+    pos, pos_type, pos_b = None, QLORA_I64, 0
     if positions is not None:
-        if positions.dtype not in (torch.int32, torch.int64):
+        if positions.dtype == torch.int32:
+            pos_type = QLORA_I32
+        elif positions.dtype != torch.int64:
             raise ValueError("rotary: positions must be int32 or int64")
         if positions.shape not in ((T,), (B, T)) or (T > 1 and positions.stride(-1) != 1):
             raise ValueError("rotary: positions must be (T,) or (B, T), contiguous along T")
+        pos = positions.data_ptr()
         pos_b = positions.stride(0) if positions.dim() == 2 else 0
-    n = 1 if k is None else 2
-    sides = (_RopeTensor * n)(_rope_side(q, qo)) if n == 1 else (_RopeTensor * n)(_rope_side(q, qo), _rope_side(k, ko))
-    with _on(q.device):
-        _check(load().qlora_rope(sides, n, QLORA_F32 if q.dtype == torch.float32 else QLORA_BF16, B, T, q.shape[-1],
-                                 config.rotary_dim, layout, th, mscale, _ptr(positions),
-                                 QLORA_I32 if positions is not None and positions.dtype == torch.int32 else QLORA_I64,
-                                 pos_b, offset, 1 if inverse else 0, _stream(stream)), "qlora_rope")
+    with _on(dev):
+        _check(load().qlora_rope(sides, 1 if k is None else 2, dtype, B, T, shape[-1], config.rotary_dim, layout, th, mscale,
+                                 pos, pos_type, pos_b, offset, 1 if inverse else 0, _stream(stream)), "qlora_rope")
     return qo, ko
 
 
@@ -529,24 +545,25 @@ def vocab_loss(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, ignore_i
         _need(dloss, torch.float32, "dloss")
         if dloss.numel() != T:
             raise ValueError(f"vocab_loss: dloss must have {T} elements")
-    dev = X.device
+    dev = X.get_device()
     dXo = dX if dX is not None else (torch.empty_like(X) if need_dx else None)
-    if dXo is not None:
+    if dX is not None:
         _need(dXo, torch.bfloat16, "dX")
         if dXo.shape != X.shape:
             raise ValueError("vocab_loss: dX must be like X")
     _same_device(dev, W=W, targets=targets, dloss=dloss, dX=dXo, workspace=workspace)
-    ws = workspace if workspace is not None else torch.empty(
-        vocab_loss_workspace_bytes(T, W.shape[0], K, dXo is not None), dtype=torch.uint8, device=dev)
+    V = W.shape[0]
+    ws = workspace if workspace is not None else torch.empty(vocab_loss_workspace_bytes(T, V, K, dXo is not None),
+                                                             dtype=torch.uint8, device=X.device)
     red = LOSS_REDUCTIONS[reduction]
-    each = torch.empty(T, dtype=torch.float32, device=dev) if red == 0 else None
-    total = torch.empty((), dtype=torch.float32, device=dev) if red else None
+    loss = torch.empty(() if red else (T,), dtype=torch.float32, device=X.device)
+    at = loss.data_ptr()
     with _on(dev):
-        _check(load().qlora_vocab_loss(_ptr(X), T, _ptr(W), W.shape[0], K, _ptr(targets),
+        _check(load().qlora_vocab_loss(X.data_ptr(), T, W.data_ptr(), V, K, targets.data_ptr(),
                                        QLORA_I32 if targets.dtype == torch.int32 else QLORA_I64, ignore_index, red,
-                                       _ptr(dloss), _ptr(each), _ptr(total), _ptr(dXo), _ptr(ws), ws.numel(),
-                                       _stream(stream)), "qlora_vocab_loss")
-    return (total if red else each), dXo
+                                       _ptr(dloss), None if red else at, at if red else None, _ptr(dXo), ws.data_ptr(),
+                                       ws.numel(), _stream(stream)), "qlora_vocab_loss")
+    return loss, dXo
 
 
 # ---- paged optimizer: AdamW step and managed-memory buffers ------------------------------------------

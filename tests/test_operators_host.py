@@ -50,7 +50,7 @@ def test_rope_refusals(q):
     def call(nx=1, dtype=1, B=1, T=4, D=128, R=128, layout=0, theta=th, mscale=1.0, pos=None, pd=1, ptr=0x100000,
              heads=2, tensors=True):
         s = (q._RopeTensor * 2)(*[(ptr, 0x200000, heads, 1024, 256, 128, 1024, 256, 128)] * 2)
-        return q.lib.qlora_rope(s if tensors else None, nx, dtype, B, T, D, R, layout, theta, mscale, pos, pd, 0, 0, 0,
+        return q.lib.qlora_rope(ctypes.cast(s, V) if tensors else None, nx, dtype, B, T, D, R, layout, theta, mscale, pos, pd, 0, 0, 0,
                                 None)
 
     assert call(tensors=False) == -1 and call(nx=0) == -1 and call(nx=3) == -1 and call(dtype=2) == -1
