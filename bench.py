@@ -663,6 +663,8 @@ def secondary_figures(q, device, reps=20, warmup=3):
 DECODE_TOKENS = (1, 4, 16)
 DECODE_WORKLOAD = ("LLaMA-65B-shaped frozen NF4 linears (N x K = 8192x8192, 22016x8192, 8192x22016), "
                    "forward only at T = 1, 4, 16 tokens, r = 64, alpha = 16")
+DECODE_WORKLOAD_SINGLE = ("LLaMA-65B-shaped frozen NF4 linears with fp32 block constants (N x K = 8192x8192, 22016x8192, "
+                          "8192x22016), forward only at T = 1, 4, 16 tokens, no adapter")
 SWEEP_SIZES = tuple(2 ** e for e in (20, 22, 24, 26, 28, 30, 31))
 
 
@@ -786,9 +788,13 @@ def run_decode(args):
     cases = []
     for i, (N, K) in enumerate(synth.LLAMA65B_SHAPES):
         W = torch.from_numpy(synth.weight_f32(N, K, seed=40 + i, tensor_id=1)).to(device)
-        nf4 = q.quantize(W)
+        single = args.weights == "single"
+        nf4 = q.quantize_single(W) if single else q.quantize(W)
         del W
-        ring = [nf4] + [nf4_copy(q, nf4) for _ in range(CHAIN_WEIGHTS - 1)]
+        if single:
+            ring = [nf4] + [q.NF4SingleWeight(nf4.codes.clone(), nf4.absmax.clone(), N, K) for _ in range(CHAIN_WEIGHTS - 1)]
+        else:
+            ring = [nf4] + [nf4_copy(q, nf4) for _ in range(CHAIN_WEIGHTS - 1)]
         A = synth.to_bf16(synth.normal_f32((RANK_R, K), 0.01, 40 + i, 3)).to(device)
         B = synth.to_bf16(synth.normal_f32((N, RANK_R), 0.01, 40 + i, 4)).to(device)
         X16 = synth.to_bf16(synth.normal_f32((max(DECODE_TOKENS), K), 1.0, 40 + i, 2)).to(device)
@@ -797,26 +803,32 @@ def run_decode(args):
             Y = torch.empty(T, N, dtype=torch.bfloat16, device=device)
             U = torch.empty(T, RANK_R, dtype=torch.bfloat16, device=device)
             ws = torch.empty(q.linear_workspace_bytes(T, N, K, RANK_R), dtype=torch.uint8, device=device)
-            fn = lambda: q.linear_fwd(X, nf4, A, B, ALPHA, out=Y, U_out=U, workspace=ws)
+
+            def call(w):
+                if single:
+                    return q.linear_single(X, w, out=Y)
+                return q.linear_fwd(X, w, A, B, ALPHA, out=Y, U_out=U, workspace=ws)
+
+            nbytes = N * K // 2 + N * K // 16 + 2 * T * (N + K) if single else gemv_bytes(T, N, K, RANK_R)
+            fn = lambda: call(nf4)
             n0 = q.kernel_launches()
             fn()
             launches = q.kernel_launches() - n0
             ms = time_calls(fn, flush, args.steps, args.warmup)
-            ms_chain = time_chain([lambda w=w: q.linear_fwd(X, w, A, B, ALPHA, out=Y, U_out=U, workspace=ws)
-                                   for w in ring], CHAIN_CALLS)
-            gbs = gemv_bytes(T, N, K, RANK_R) / (ms / 1e3) / 1e9
+            ms_chain = time_chain([lambda w=w: call(w) for w in ring], CHAIN_CALLS)
+            gbs = nbytes / (ms / 1e3) / 1e9
             cases.append({"N": N, "K": K, "T": T, "us": round(ms * 1e3, 2), "GB/s": round(gbs, 1),
-                          "frac": round(gbs / peaks["hbm_gbs"], 4), "bytes": int(gemv_bytes(T, N, K, RANK_R)),
+                          "frac": round(gbs / peaks["hbm_gbs"], 4), "bytes": int(nbytes),
                           "launches_per_call": launches,
-                          "chain": chain_entry(ms_chain, gemv_bytes(T, N, K, RANK_R), peaks)})
+                          "chain": chain_entry(ms_chain, nbytes, peaks)})
         del ring
     status = q.get_status()
     gm = math.exp(sum(math.log(c["GB/s"]) for c in cases) / len(cases))
     print(json.dumps({"metric": "QLoRA decode-shaped linear forward, HBM GB/s (geomean over cases)",
                       "value": round(gm, 1), "unit": "GB/s", "n_gpus": 1, "steps": args.steps,
                       "warmup": args.warmup, "higher_is_better": True, "dtype": "bf16", "data": "synthetic",
-                      "config": {"workload": DECODE_WORKLOAD, "r": RANK_R, "alpha": ALPHA,
-                                 "l2": L2_NOTE},
+                      "config": {"workload": DECODE_WORKLOAD_SINGLE if args.weights == "single" else DECODE_WORKLOAD,
+                                 **({} if args.weights == "single" else {"r": RANK_R, "alpha": ALPHA}), "l2": L2_NOTE},
                       "roofline": {"bound": "hbm", "unit": "GB/s", "peak": peaks["hbm_gbs"],
                                    "peak_source": f"{kind} (HBM copy)", "achieved": round(gm, 1),
                                    "frac": round(gm / peaks["hbm_gbs"], 4)},
@@ -1146,9 +1158,12 @@ def run_paged_adamw(args):
     return 0
 
 
-def build_decoder(layers, d, ffn, heads, vocab, r, gen, device):
-    """A LLaMA-shaped decoder whose seven linears per layer are QLoRALinear modules (random init)."""
+def build_decoder(layers, d, ffn, heads, vocab, r, gen, device, positions=None, fused_loss=False):
+    """A LLaMA-shaped decoder whose seven linears per layer are QLoRALinear modules (random init). positions: a
+    RotaryConfig that turns queries and keys by their tokens' positions (None: no positions). fused_loss: the
+    library's vocabulary loss at the end instead of torch's logits and cross entropy."""
     import torch
+    from bit_nf4_quantized_14_b200 import autograd
     from bit_nf4_quantized_14_b200.autograd import QLoRALinear
 
     def lin(n, k):
@@ -1168,8 +1183,10 @@ def build_decoder(layers, d, ffn, heads, vocab, r, gen, device):
         def forward(self, h):
             T = h.shape[0]
             x = rms(h, self.n1)
-            q = self.q(x).view(T, heads, d // heads).transpose(0, 1)
-            k = self.k(x).view(T, heads, d // heads).transpose(0, 1)
+            q, k = self.q(x).view(T, heads, d // heads), self.k(x).view(T, heads, d // heads)
+            if positions is not None:
+                q, k = autograd.rotary(q, k, positions)
+            q, k = q.transpose(0, 1), k.transpose(0, 1)
             v = self.v(x).view(T, heads, d // heads).transpose(0, 1)
             a = torch.nn.functional.scaled_dot_product_attention(q[None], k[None], v[None], is_causal=True)[0]
             h = h + self.o(a.transpose(0, 1).reshape(T, d))
@@ -1192,6 +1209,8 @@ def build_decoder(layers, d, ffn, heads, vocab, r, gen, device):
             h = self.emb[ids]
             for layer in self.layers:
                 h = layer(h)
+            if fused_loss:
+                return autograd.vocab_loss(rms(h, self.nf), self.head, targets)
             logits = rms(h, self.nf) @ self.head.t()
             return torch.nn.functional.cross_entropy(logits.float(), targets)
 
@@ -1205,7 +1224,9 @@ def run_llama65b_train(args):
     gen = torch.Generator(device=device)
     gen.manual_seed(66)
     vocab, T = 32000, LLAMA65B_TOKENS
-    model = build_decoder(LLAMA65B_LAYERS, 8192, 22016, 64, vocab, RANK_R, gen, device)
+    positions = q.RotaryConfig(8192 // 64) if args.rope else None
+    model = build_decoder(LLAMA65B_LAYERS, 8192, 22016, 64, vocab, RANK_R, gen, device, positions=positions,
+                          fused_loss=args.loss == "vocab")
     params = [p for p in model.parameters() if p.requires_grad]
     if args.optimizer == "torch":
         opt = torch.optim.AdamW(params, lr=2e-4, weight_decay=0.0, fused=True)
@@ -1268,6 +1289,9 @@ def run_llama65b_train(args):
                                     "paged_evicted_prefetch": "PagedAdamW, moments evicted at the start of every "
                                                               "step on a side stream and prefetched back there "
                                                               "while the forward and backward run"}[args.optimizer],
+                      "positions": "rotary (library kernel)" if args.rope else "none",
+                      "loss": "library vocabulary loss" if args.loss == "vocab" else "torch logits + cross entropy",
+                      "peak_memory_gib": round(torch.cuda.max_memory_allocated() / 2 ** 30, 2),
                       "library_linears_ms_per_step": round(lin_ms, 3),
                       "library_linears_share": round(lin_ms / ms, 4),
                       "final_loss": float(loss.item()), "gpu_launches": int(launches), "clocks": clk,
@@ -1288,6 +1312,13 @@ def main(argv=None):
     ap.add_argument("--optimizer", choices=["torch", "paged", "paged_evicted", "paged_evicted_prefetch"],
                     default="torch",
                     help="with --workload llama65b_train: the adapters' optimizer")
+    ap.add_argument("--rope", action="store_true",
+                    help="with --workload llama65b_train: turn queries and keys by their positions (library kernel)")
+    ap.add_argument("--loss", choices=["torch", "vocab"], default="torch",
+                    help="with --workload llama65b_train: torch's logits and cross entropy, or the library's vocabulary loss")
+    ap.add_argument("--weights", choices=["double", "single"], default="double",
+                    help="with --workload decode: NF4 with double-quantized constants and LoRA (linear_fwd), or with fp32 "
+                         "constants and no adapter (linear_single)")
     ap.add_argument("--workload", choices=["llama7b_step", "decode", "codec_sweep", "llama65b_linears",
                                            "llama65b_train", "codebook_study", "paged_adamw", "flush_check"],
                     default="llama7b_step",

@@ -471,37 +471,42 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, config: RotaryConfig, positi
     back, which is the gradient. out: a pair of tensors like (q, k), the inputs themselves for in place.
     Returns (q', k')."""
     shape = q.shape
+    nd = len(shape)
     dtype = _ROPE_TYPES.get(q.dtype)
-    if len(shape) not in (3, 4) or dtype is None or not q.is_cuda:
+    if nd not in (3, 4) or dtype is None or not q.is_cuda:
         raise ValueError("rotary: q must be a (T, heads, dim) or (B, T, heads, dim) CUDA tensor of float32 or bfloat16")
     dev = q.get_device()
     qo, ko = (None, None) if out is None else out
-    qo = torch.empty_like(q) if qo is None else qo
-    if qo.shape != shape or qo.dtype != q.dtype:
+    if qo is None:
+        qo = torch.empty_like(q)
+    elif qo.shape != shape or qo.dtype != q.dtype:
         raise ValueError("rotary: out must match the inputs")
     sides = _rope_side(q, qo)
     if k is not None:
-        if k.dtype != q.dtype or k.shape[:-2] != shape[:-2] or k.shape[-1] != shape[-1]:
+        ks = k.shape
+        if k.dtype != q.dtype or len(ks) != nd or ks[0] != shape[0] or ks[-1] != shape[-1] or (nd == 4 and ks[1] != shape[1]):
             raise ValueError("rotary: k must match q in type, tokens and head size")
-        ko = torch.empty_like(k) if ko is None else ko
-        if ko.shape != k.shape or ko.dtype != k.dtype:
+        if ko is None:
+            ko = torch.empty_like(k)
+        elif ko.shape != ks or ko.dtype != k.dtype:
             raise ValueError("rotary: out must match the inputs")
         sides += _rope_side(k, ko)
     else:
         ko = None
     _same_device(dev, k=k, out=qo, k_out=ko, positions=positions)
     th, mscale, layout = _rope_setup(config)
-    B, T = shape[:2] if len(shape) == 4 else (1, shape[0])
+    B, T = (shape[0], shape[1]) if nd == 4 else (1, shape[0])
     pos, pos_type, pos_b = None, QLORA_I64, 0
     if positions is not None:
         if positions.dtype == torch.int32:
             pos_type = QLORA_I32
         elif positions.dtype != torch.int64:
             raise ValueError("rotary: positions must be int32 or int64")
-        if positions.shape not in ((T,), (B, T)) or (T > 1 and positions.stride(-1) != 1):
+        ps, pst = positions.shape, positions.stride()
+        if len(ps) not in (1, 2) or ps[-1] != T or (len(ps) == 2 and ps[0] != B) or (T > 1 and pst[-1] != 1):
             raise ValueError("rotary: positions must be (T,) or (B, T), contiguous along T")
         pos = positions.data_ptr()
-        pos_b = positions.stride(0) if positions.dim() == 2 else 0
+        pos_b = pst[0] if len(ps) == 2 else 0
     with _on(dev):
         _check(load().qlora_rope(sides, 1 if k is None else 2, dtype, B, T, shape[-1], config.rotary_dim, layout, th, mscale,
                                  pos, pos_type, pos_b, offset, 1 if inverse else 0, _stream(stream)), "qlora_rope")
