@@ -864,13 +864,13 @@ int launch_codebook_linear4(ClParams p, const CodebookArg& cb, int sms, cudaStre
   const bool vec = p.nkb % 4 == 0;
   auto kern = vec ? codebook_linear4_kernel<NT, true> : codebook_linear4_kernel<NT, false>;
   CUtensorMap tc, ts = {};
-  if (!make_tmap_t(&tc, p.codes, TmType::kU8, p.nkb * int64_t(32), p.N, p.nkb * int64_t(32), 128, 32, true) ||
-      (vec && !make_tmap_t(&ts, p.absmax, TmType::kF32, p.nkb, p.N, p.nkb, 4, 32, false)))
+  if (!make_tmap_t(&tc, p.codes, TmType::kU8, p.nkb * int64_t(32), p.N, p.nkb * int64_t(32), 128, 16 * C4<NT>::ST, true) ||
+      (vec && !make_tmap_t(&ts, p.absmax, TmType::kF32, p.nkb, p.N, p.nkb, 4, 16 * C4<NT>::ST, false)))
     return cuda_fail(cudaGetLastError(), "tensor-map encode", __LINE__);
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kC4Smem) != cudaSuccess)
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C4<NT>::SMEM) != cudaSuccess)
     return cuda_fail(cudaGetLastError(), "cudaFuncSetAttribute", __LINE__);
   p.pairs = std::max(1, std::min(p.tiles, sms / 2));
-  kern<<<2 * p.pairs, kC4Warps * 32, kC4Smem, st>>>(tc, ts, p, cb);
+  kern<<<2 * p.pairs, C4<NT>::WARPS * 32, C4<NT>::SMEM, st>>>(tc, ts, p, cb);
   return launched();
 }
 

@@ -461,21 +461,24 @@ __global__ void __launch_bounds__(kC1Warps * 32, 1)
 // per warp (32 rows x 128 bytes, 128-byte swizzle; quad g takes row 2 (g % 4) + g / 4 of each 8, whose 8-byte
 // loads then hit distinct banks). (Boxes of 16 rows x 64 or 128 bytes with 4-byte copies of the constants took
 // 51 us for 16 tokens through 8192 x 22016, 32 us of it for the stream alone.)
-constexpr int kC4Warps = 8, kC4Tiles = 4;
-constexpr int kC4CodeBytes = 32 * 128, kC4ScaleBytes = 32 * 4 * 4;
+constexpr int kC4Tiles = 4;
 constexpr uint32_t kC4Slots = 2u << 16;
-constexpr uint32_t kC4Scales = kC4Slots + kC4Warps * 2 * kC4CodeBytes;
-constexpr uint32_t kC4Bars = kC4Scales + kC4Warps * 2 * kC4ScaleBytes;
-constexpr int kC4Smem = static_cast<int>(kC4Bars) + kC4Warps * 2 * 8;
-__host__ __device__ constexpr int c4_peer_bytes(int NT) { return kC4Tiles * 16 * 8 * NT * 4; }
-static_assert(kC4Smem <= 227 * 1024 && kClBaseMax + (kC4Warps + 1) * c4_peer_bytes(2) <= 65536, "shared memory");
+template <int NT> struct C4 {
+  static constexpr int WARPS = NT == 1 ? 16 : 8, ST = NT == 1 ? 1 : 2;      // warps; tiles per slot
+  static constexpr int CODE_BYTES = ST * 16 * 128, SCALE_BYTES = ST * 16 * 4 * 4;
+  static constexpr uint32_t SCALES = kC4Slots + WARPS * 2 * CODE_BYTES, BARS = SCALES + WARPS * 2 * SCALE_BYTES;
+  static constexpr int SMEM = static_cast<int>(BARS) + WARPS * 2 * 8;
+  static constexpr int SUM_BYTES = kC4Tiles * 16 * 8 * NT * 4;              // a warp's sums of a pass
+  static_assert(SMEM <= 227 * 1024 && kClBaseMax + (WARPS + 1) * SUM_BYTES <= 65536, "shared memory");
+};
 
 // VEC: constants by TMA (K % 256 == 0), else by 4-byte copies.
 template <int NT, bool VEC>
-__global__ void __launch_bounds__(kC4Warps * 32, 1) __cluster_dims__(2, 1, 1)
+__global__ void __launch_bounds__(C4<NT>::WARPS * 32, 1) __cluster_dims__(2, 1, 1)
     codebook_linear4_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmS, const __grid_constant__ ClParams p,
                             const __grid_constant__ CodebookArg cb) {
-  constexpr int TT = 8 * NT;
+  using C = C4<NT>;
+  constexpr int TT = 8 * NT, WARPS = C::WARPS, ST = C::ST;
   extern __shared__ __align__(1024) uint8_t cl_smem[];
   const uint32_t base = smem_u32(cl_smem), window = base & 0xFF000000u;
   const uint32_t table = window | kClTable;
@@ -486,10 +489,10 @@ __global__ void __launch_bounds__(kC4Warps * 32, 1) __cluster_dims__(2, 1, 1)
     if (threadIdx.x == 0) raise_status(kStatusTimeout);
     return;
   }
-  const uint32_t slots = (window | kC4Slots) + warp * 2 * kC4CodeBytes;
-  const uint32_t scales = window + kC4Scales + warp * 2 * kC4ScaleBytes;
-  const uint32_t bars = window + kC4Bars + warp * 2 * 8;
-  const uint32_t red = base + c4_peer_bytes(NT);     // the warps' sums; the pair's second half hands over at base
+  const uint32_t slots = (window | kC4Slots) + warp * 2 * C::CODE_BYTES;
+  const uint32_t scales = window + C::SCALES + warp * 2 * C::SCALE_BYTES;
+  const uint32_t bars = window + C::BARS + warp * 2 * 8;
+  const uint32_t red = base + C::SUM_BYTES;     // the warps' sums; the pair's second half hands over at base
   if (lane == 0) {
     for (int s = 0; s < 2; ++s)
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bars + 8 * s), "r"(VEC ? 1 : 33));
@@ -506,20 +509,20 @@ __global__ void __launch_bounds__(kC4Warps * 32, 1) __cluster_dims__(2, 1, 1)
 
   const int t_lo = static_cast<int>(static_cast<int64_t>(pair) * p.tiles / p.pairs);
   const int t_hi = static_cast<int>(static_cast<int64_t>(pair + 1) * p.tiles / p.pairs);
-  const int part = rank * kC4Warps + warp;           // this warp's share of the blocks
+  const int part = rank * WARPS + warp;           // this warp's share of the blocks
   const int units = (p.nkb + 3) / 4;                 // of 256 elements
-  const int u_lo = part * units / (2 * kC4Warps), nu = (part + 1) * units / (2 * kC4Warps) - u_lo;
+  const int u_lo = part * units / (2 * WARPS), nu = (part + 1) * units / (2 * WARPS) - u_lo;
   uint32_t in_slot = 0, slot = 0, phase = 0;
   bool ok = true;
   for (int t0 = t_lo; t0 < t_hi; t0 += kC4Tiles) {
-    const int nt = min(kC4Tiles, t_hi - t0), halves = (nt + 1) / 2, n = nu * halves;
-    int issued = 0, done = 0, fu = u_lo, fh = 0;     // what to fetch next: unit fu, tiles 2 fh and 2 fh + 1
+    const int nt = min(kC4Tiles, t_hi - t0), groups = (nt + ST - 1) / ST, n = nu * groups;
+    int issued = 0, done = 0, fu = u_lo, fh = 0;     // what to fetch next: unit fu, tiles from ST fh
     auto fetch = [&]() {
-      const uint32_t bar = bars + 8 * in_slot, sdst = scales + in_slot * kC4ScaleBytes;
-      const int row = (t0 + 2 * fh) * 16;
+      const uint32_t bar = bars + 8 * in_slot, sdst = scales + in_slot * C::SCALE_BYTES;
+      const int row = (t0 + ST * fh) * 16;
       if constexpr (!VEC) {
 #pragma unroll
-        for (int e = lane; e < 128; e += 32) {
+        for (int e = lane; e < ST * 64; e += 32) {
           const int r = row + (e >> 2), kb = 4 * fu + (e & 3);
           const bool in = r < p.N && kb < p.nkb;
           c1_cp4(sdst + 4u * e, p.absmax + (in ? static_cast<int64_t>(r) * p.nkb + kb : 0), in ? 4u : 0u);
@@ -527,13 +530,13 @@ __global__ void __launch_bounds__(kC4Warps * 32, 1) __cluster_dims__(2, 1, 1)
         c1_cp_arrive(bar);
       }
       if (lane == 0) {
-        c1_expect(bar, kC4CodeBytes + (VEC ? kC4ScaleBytes : 0));
-        c1_tma(slots + in_slot * kC4CodeBytes, &tmC, bar, fu * 128, row);
+        c1_expect(bar, C::CODE_BYTES + (VEC ? C::SCALE_BYTES : 0));
+        c1_tma(slots + in_slot * C::CODE_BYTES, &tmC, bar, fu * 128, row);
         if constexpr (VEC) c1_tma(sdst, &tmS, bar, fu * 4, row);
       }
       in_slot ^= 1;
       ++issued;
-      if (++fh == halves) { fh = 0; ++fu; }
+      if (++fh == groups) { fh = 0; ++fu; }
     };
     if (n > 0) fetch();
     if (n > 1) fetch();
@@ -555,9 +558,9 @@ __global__ void __launch_bounds__(kC4Warps * 32, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
       for (int t = 0; t < kC4Tiles; ++t) {
         if (t >= nt || !ok) break;
-        if (t % 2 == 0 && !__all_sync(0xffffffffu, mbar_wait_addr(bars + 8 * slot, phase))) { ok = false; break; }
-        const uint32_t at = slots + slot * kC4CodeBytes + 2048u * (t & 1) + 128u * gr + 8u * (j & 1);
-        const uint32_t sa = scales + slot * kC4ScaleBytes + 256u * (t & 1) + 16u * gr;
+        if (t % ST == 0 && !__all_sync(0xffffffffu, mbar_wait_addr(bars + 8 * slot, phase))) { ok = false; break; }
+        const uint32_t at = slots + slot * C::CODE_BYTES + 2048u * (t % ST) + 128u * gr + 8u * (j & 1);
+        const uint32_t sa = scales + slot * C::SCALE_BYTES + 256u * (t % ST) + 16u * gr;
         uint2 w[4][2];
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
@@ -566,7 +569,7 @@ __global__ void __launch_bounds__(kC4Warps * 32, 1) __cluster_dims__(2, 1, 1)
           w[b][1] = dc_ld64(c + 1024);
         }
         const uint4 f0 = dc_ld128(sa), f1 = dc_ld128(sa + 128);
-        if (t % 2 == 1 || t == nt - 1) {
+        if (t % ST == ST - 1 || t == nt - 1) {
           __syncwarp();                              // the slot has been read
           slot ^= 1;
           phase ^= slot ^ 1;
@@ -610,7 +613,7 @@ __global__ void __launch_bounds__(kC4Warps * 32, 1) __cluster_dims__(2, 1, 1)
     for (int t = 0; t < kC4Tiles; ++t)
 #pragma unroll
       for (int m = 0; m < NT; ++m) {
-        const uint32_t to = red + static_cast<uint32_t>(warp) * c4_peer_bytes(NT) + 4u * ((t * 16 + gr) * TT + 8 * m + 2 * j);
+        const uint32_t to = red + static_cast<uint32_t>(warp) * C::SUM_BYTES + 4u * ((t * 16 + gr) * TT + 8 * m + 2 * j);
         cl_sts2(to, acc[t][m][0], acc[t][m][1]);
         cl_sts2(to + 4u * 8 * TT, acc[t][m][2], acc[t][m][3]);
       }
@@ -618,7 +621,7 @@ __global__ void __launch_bounds__(kC4Warps * 32, 1) __cluster_dims__(2, 1, 1)
     auto mine = [&](int e) {
       float sum = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kC4Warps; ++w) sum += cl_lds(red + static_cast<uint32_t>(w) * c4_peer_bytes(NT) + 4u * e);
+      for (int w = 0; w < WARPS; ++w) sum += cl_lds(red + static_cast<uint32_t>(w) * C::SUM_BYTES + 4u * e);
       return sum;
     };
     if (rank == 1)
