@@ -833,17 +833,6 @@ int launch_pass1_single(const void* w, int w_dtype, int64_t n, uint8_t* codes, f
 static_assert(kStatOut == QLORA_CODEBOOK_STATS_LEN, "codebook statistics layout");
 int64_t stat_ctas(int64_t n) { return std::min<int64_t>(cdiv(cdiv(n, kStepElems), kStatThreads / 32), kStatMaxCtas); }
 // ---- product of a few tokens with a codebook-quantized weight --------------------------------------
-template <int NT>
-int launch_codebook_linear(ClParams p, const CodebookArg& cb, int sms, cudaStream_t st) {
-  auto kern = codebook_linear_kernel<NT>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, cl_smem_bytes(NT)) != cudaSuccess)
-    return cuda_fail(cudaGetLastError(), "cudaFuncSetAttribute", __LINE__);
-  p.pairs = std::max(1, std::min(p.tiles, sms / 2));
-  const dim3 grid(2u * p.pairs, static_cast<unsigned>(cdiv(p.T, 8 * NT)));
-  kern<<<grid, kClWarps * 32, cl_smem_bytes(NT), st>>>(p, cb);
-  return launched();
-}
-
 int launch_codebook_linear1(ClParams p, const CodebookArg& cb, int sms, cudaStream_t st) {
   const bool vec = p.nkb % 4 == 0;
   auto kern = vec ? codebook_linear1_kernel<true> : codebook_linear1_kernel<false>;
@@ -862,15 +851,19 @@ int launch_codebook_linear1(ClParams p, const CodebookArg& cb, int sms, cudaStre
 template <int NT>
 int launch_codebook_linear4(ClParams p, const CodebookArg& cb, int sms, cudaStream_t st) {
   const bool vec = p.nkb % 4 == 0;
-  auto kern = vec ? codebook_linear4_kernel<NT, true> : codebook_linear4_kernel<NT, false>;
+  const bool pair = 2 * p.tiles <= sms;       // half of the SMs or more would have no tile
+  auto kern = pair ? (vec ? codebook_linear4_pair_kernel<NT, true> : codebook_linear4_pair_kernel<NT, false>)
+                   : (vec ? codebook_linear4_kernel<NT, true> : codebook_linear4_kernel<NT, false>);
   CUtensorMap tc, ts = {};
   if (!make_tmap_t(&tc, p.codes, TmType::kU8, p.nkb * int64_t(32), p.N, p.nkb * int64_t(32), 128, 16 * C4<NT>::ST, true) ||
       (vec && !make_tmap_t(&ts, p.absmax, TmType::kF32, p.nkb, p.N, p.nkb, 4, 16 * C4<NT>::ST, false)))
     return cuda_fail(cudaGetLastError(), "tensor-map encode", __LINE__);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C4<NT>::SMEM) != cudaSuccess)
     return cuda_fail(cudaGetLastError(), "cudaFuncSetAttribute", __LINE__);
-  p.pairs = std::max(1, std::min(p.tiles, sms / 2));
-  kern<<<2 * p.pairs, C4<NT>::WARPS * 32, C4<NT>::SMEM, st>>>(tc, ts, p, cb);
+  p.workers = std::min(p.tiles, sms);
+  const dim3 grid(static_cast<unsigned>((pair ? 2 : 1) * p.workers), static_cast<unsigned>(cdiv(p.T, 8 * NT)));
+  if (launch_pdl_smem(kern, grid, C4<NT>::WARPS * 32, C4<NT>::SMEM, st, tc, ts, p, cb) != cudaSuccess)
+    return cuda_fail(cudaGetLastError(), "cudaLaunchKernelEx", __LINE__);
   return launched();
 }
 
@@ -1432,8 +1425,7 @@ int qlora_codebook_linear(const void* X, int64_t T, const void* codes, const flo
   // one or two tokens whose X fits in shared memory (K up to 24,500, or 12,200 for two)
   if (T <= kC1Tokens && c1_x_bytes(T, K / 64) <= kC1XBytes) return launch_codebook_linear1(p, cb, sms, st);
   if (T <= 8) return launch_codebook_linear4<1>(p, cb, sms, st);
-  if (T <= 16) return launch_codebook_linear4<2>(p, cb, sms, st);
-  return launch_codebook_linear<4>(p, cb, sms, st);   // above 32: two groups of tokens, the second's weights from L2
+  return launch_codebook_linear4<2>(p, cb, sms, st);
 }
 
 int qlora_rope_frequencies(int rotary_dim, double base, int scaling, double factor, double original_length,

@@ -8,10 +8,9 @@
 // index is permuted alike on both operands, so lane j of a quad holds elements 16 j .. 16 j + 15: 8 code bytes and
 // 32 bytes of X in a row. The block's constant multiplies the fp32 result of its four MMAs, so the only rounding
 // of a weight is its level's to bf16 (a relative 2^-8 at most), as in the T <= 16 forward of the double-quantized layer.
-// Warps run without barriers: a pair of CTAs (a cluster, each CTA with half of the contraction: the finer cut
-// fills 148 SMs evenly) owns a run of row tiles, cut evenly over its warps wherever a tile ends, and each lane
-// keeps the codes and constants of 8 blocks in flight (64 KB per SM). Where a warp leaves a row tile its fp32
-// sums go to shared memory, and at the end of a pass they are added in a fixed order: deterministic.
+// Two kernels: one for one or two tokens, one for up to 16 (more run as groups of 16, whose weights after the first
+// come from L2 where they fit). In both every warp streams its own share of a CTA's rows or contraction with no
+// barrier between warps, and fp32 sums are added in a fixed order: deterministic.
 #pragma once
 
 #include "codec.cuh"
@@ -20,42 +19,23 @@
 
 namespace qnf4 {
 
-constexpr int kClWarps = 16;
 constexpr int kClMaxTokens = 64;
-constexpr int kClDepth = 8;              // blocks of 64 whose codes and constants each lane holds in flight
-// Shared memory: a CTA pair's second half hands its sums over below the table; the table (256 entries of 256
-// bytes, the lane copies in the first 128) sits at shared address 64 KB, so one byte permute forms a lookup's
-// address; the warps' sums of a pass lie above it.
-constexpr uint32_t kClTable = 1u << 16, kClRed = 2u << 16;
+// Measured (a weight in HBM, calls back to back): 22016 x 8192 at one token 24 us (4.2 TB/s), 4 tokens 31, 16
+// tokens 43; 8192 x 8192 at one token 12.5 us. The plain copy's rate would be 15.5 and 5.8 us.
+//
+// Shared memory: the table (256 entries of 256 bytes, the lane copies in the first 128) sits at shared address
+// 64 KB, so one byte permute forms a lookup's address; the stream's slots lie above it, sums (and X) below.
+constexpr uint32_t kClTable = 1u << 16;
 constexpr int kClBaseMax = 4096;         // where the dynamic shared memory may begin, at most
-__host__ __device__ constexpr int cl_pass_tiles(int NT) { return NT <= 2 ? 32 : 16; }
-__host__ __device__ constexpr int cl_segments(int NT) { return cl_pass_tiles(NT) / kClWarps + 2; }   // row tiles one warp may touch in a pass
-__host__ __device__ constexpr int cl_red_bytes(int NT) { return kClWarps * cl_segments(NT) * 16 * 8 * NT * 4; }
-__host__ __device__ constexpr int cl_smem_bytes(int NT) { return static_cast<int>(kClRed) + cl_red_bytes(NT); }
-static_assert(cl_smem_bytes(1) <= 227 * 1024 && cl_smem_bytes(2) <= 227 * 1024 && cl_smem_bytes(4) <= 227 * 1024,
-              "shared memory per CTA");
-static_assert(kClBaseMax + cl_pass_tiles(2) * 16 * 16 * 4 <= 65536 && cl_pass_tiles(4) * 16 * 32 * 4 + kClBaseMax <= 65536,
-              "the handed-over sums lie below the table");
 
 struct ClParams {
-  int T, N, nkb, tiles, pairs;           // pairs: CTA pairs per token group
+  int T, N, nkb, tiles, workers;         // tiles of rows, and the CTAs (or pairs) that share them
   const __nv_bfloat16* X;
   const uint8_t* codes;
   const float* absmax;
   __nv_bfloat16* Y;
 };
 
-// Codes are read once: not kept in L1, and fetched from HBM in runs of 256 bytes of a row.
-__device__ __forceinline__ uint2 cl_ld_codes(const uint8_t* p) {
-  uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
-}
-__device__ __forceinline__ float cl_ld_scale(const float* p) {
-  float v;
-  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
-  return v;
-}
 __device__ __forceinline__ void cl_cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -75,172 +55,14 @@ __device__ __forceinline__ void cl_sts2(uint32_t addr, float a, float b) {
   asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(a), "f"(b) : "memory");
 }
 
-template <int NT>   // token tiles of 8; blockIdx.y: groups of 8 NT tokens
-__global__ void __launch_bounds__(kClWarps * 32, 1) __cluster_dims__(2, 1, 1)
-    codebook_linear_kernel(const __grid_constant__ ClParams p, const __grid_constant__ CodebookArg cb) {
-  constexpr int PT = cl_pass_tiles(NT), SEG = cl_segments(NT), TT = 8 * NT, D = kClDepth;
-  extern __shared__ __align__(1024) uint8_t cl_smem[];
-  // a CTA's shared addresses lie in its own window of the cluster's: the layout's are relative to that
-  const uint32_t base = smem_u32(cl_smem), window = base & 0xFF000000u;
-  const uint32_t table = window | kClTable, redu = window | kClRed;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, j = lane & 3;
-  const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1;
-  const int tok0 = blockIdx.y * TT, T = min(TT, p.T - tok0);
-  const __nv_bfloat16* X = p.X + static_cast<int64_t>(tok0) * p.nkb * 64;
-  if (base - window > kClBaseMax) {      // the table's address needs a low base; the same in both CTAs of the pair
-    if (threadIdx.x == 0) raise_status(kStatusTimeout);
-    return;
-  }
-  for (int i = threadIdx.x; i < 256 * 32; i += blockDim.x) {
-    const uint32_t v = pack_bf16x2(cb.levels[i >> 9], cb.levels[(i >> 5) & 15]);
-    asm volatile("st.shared.u32 [%0], %1;" ::"r"(table + (static_cast<uint32_t>(i >> 5) << 8) + 4u * (i & 31)), "r"(v)
-                 : "memory");
-  }
-  cl_cluster_sync();                     // the table is complete; the other CTA of the pair runs
-  const uint32_t lanebyte = table | (4u * lane);
-  const int K = p.nkb * 64;
-  const int64_t row_bytes = K / 2;
-
-  // this pair's row tiles, and this CTA's half of the contraction
-  const int t_lo = static_cast<int>(static_cast<int64_t>(pair) * p.tiles / p.pairs);
-  const int t_hi = static_cast<int>(static_cast<int64_t>(pair + 1) * p.tiles / p.pairs);
-  const int half = (p.nkb + 1) / 2;
-  const int kb_lo = rank ? half : 0, nb = rank ? p.nkb - half : half;
-
-  for (int t0 = t_lo; t0 < t_hi; t0 += PT) {
-    // the pass's blocks, tile by tile, in one run cut evenly over the warps
-    const int nt = min(PT, t_hi - t0);
-    const int total = nt * nb, chunk = max(1, (total + kClWarps - 1) / kClWarps);
-    const int b0 = min(total, warp * chunk), n = min(total, b0 + chunk) - b0;
-    if (n > 0) {
-      // load cursor: the block to fetch next
-      int lt = b0 / nb, lk = b0 - lt * nb;
-      const uint8_t *c0, *c1;
-      const float *a0, *a1;
-      auto aim = [&]() {
-        const int64_t r0 = min((t0 + lt) * 16 + g, p.N - 1), r1 = min((t0 + lt) * 16 + g + 8, p.N - 1);
-        c0 = p.codes + r0 * row_bytes + 32 * (kb_lo + lk) + 8 * j;
-        c1 = p.codes + r1 * row_bytes + 32 * (kb_lo + lk) + 8 * j;
-        a0 = p.absmax + r0 * p.nkb + kb_lo + lk;
-        a1 = p.absmax + r1 * p.nkb + kb_lo + lk;
-      };
-      aim();
-      uint2 w0[D], w1[D];
-      float s0[D], s1[D];
-      auto fetch = [&](uint2& x0, uint2& x1, float& y0, float& y1) {
-        x0 = cl_ld_codes(c0);
-        x1 = cl_ld_codes(c1);
-        y0 = cl_ld_scale(a0);
-        y1 = cl_ld_scale(a1);
-        if (++lk == nb) {
-          lk = 0;
-          ++lt;
-          aim();
-        } else {
-          c0 += 32; c1 += 32; ++a0; ++a1;
-        }
-      };
-#pragma unroll
-      for (int s = 0; s < D; ++s)
-        if (s < n) fetch(w0[s], w1[s], s0[s], s1[s]);
-
-      int ck = b0 - (b0 / nb) * nb, seg = 0;
-      float acc[NT][4] = {};
-      auto flush = [&]() {             // this warp's sums of a row tile
-        const uint32_t red = redu + static_cast<uint32_t>((warp * SEG + seg) * 16 * TT * 4);
-#pragma unroll
-        for (int m = 0; m < NT; ++m) {
-          cl_sts2(red + 4u * (g * TT + 8 * m + 2 * j), acc[m][0], acc[m][1]);
-          cl_sts2(red + 4u * ((g + 8) * TT + 8 * m + 2 * j), acc[m][2], acc[m][3]);
-          acc[m][0] = acc[m][1] = acc[m][2] = acc[m][3] = 0.0f;
-        }
-        ++seg;
-      };
-      for (int i = 0; i < n; i += D) {
-#pragma unroll
-        for (int s = 0; s < D; ++s) {
-          if (i + s < n) {
-            const __nv_bfloat16* xk = X + static_cast<int64_t>(64) * (kb_lo + ck) + 16 * j;
-            uint4 x[NT][2];
-#pragma unroll
-            for (int m = 0; m < NT; ++m) {
-              x[m][0] = x[m][1] = make_uint4(0, 0, 0, 0);
-              if (8 * m + g < T) {
-                const uint4* xp = reinterpret_cast<const uint4*>(xk + static_cast<int64_t>(8 * m + g) * K);
-                x[m][0] = __ldg(xp);
-                x[m][1] = __ldg(xp + 1);
-              }
-            }
-            uint32_t a[16];
-            a[0] = dc_pair<0>(w0[s].x, lanebyte);  a[1] = dc_pair<0>(w1[s].x, lanebyte);
-            a[2] = dc_pair<1>(w0[s].x, lanebyte);  a[3] = dc_pair<1>(w1[s].x, lanebyte);
-            a[4] = dc_pair<2>(w0[s].x, lanebyte);  a[5] = dc_pair<2>(w1[s].x, lanebyte);
-            a[6] = dc_pair<3>(w0[s].x, lanebyte);  a[7] = dc_pair<3>(w1[s].x, lanebyte);
-            a[8] = dc_pair<0>(w0[s].y, lanebyte);  a[9] = dc_pair<0>(w1[s].y, lanebyte);
-            a[10] = dc_pair<1>(w0[s].y, lanebyte); a[11] = dc_pair<1>(w1[s].y, lanebyte);
-            a[12] = dc_pair<2>(w0[s].y, lanebyte); a[13] = dc_pair<2>(w1[s].y, lanebyte);
-            a[14] = dc_pair<3>(w0[s].y, lanebyte); a[15] = dc_pair<3>(w1[s].y, lanebyte);
-            const float f0 = s0[s], f1 = s1[s];
-            if (i + s + D < n) fetch(w0[s], w1[s], s0[s], s1[s]);
-#pragma unroll
-            for (int m = 0; m < NT; ++m) {
-              float d[4] = {};
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                dc_mma(d[0], d[1], d[2], d[3], a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3],
-                       dc_word(x[m][q >> 1], 2 * (q & 1)), dc_word(x[m][q >> 1], 2 * (q & 1) + 1));
-              acc[m][0] = fmaf(f0, d[0], acc[m][0]);
-              acc[m][1] = fmaf(f0, d[1], acc[m][1]);
-              acc[m][2] = fmaf(f1, d[2], acc[m][2]);
-              acc[m][3] = fmaf(f1, d[3], acc[m][3]);
-            }
-            if (++ck == nb) {
-              ck = 0;
-              flush();
-            }
-          }
-        }
-      }
-      if (ck != 0) flush();
-    }
-    __syncthreads();
-    // a tile's sums: the warps that cover it, in order, then the pair's second half
-    auto mine = [&](int tile, int e) {
-      float sum = 0.0f;
-      if (nb > 0) {
-        const int first = tile * nb / chunk, last = ((tile + 1) * nb - 1) / chunk;
-        for (int w = first; w <= last; ++w) {
-          const int sg = tile - (w * chunk) / nb;
-          sum += cl_lds(redu + 4u * static_cast<uint32_t>((w * SEG + sg) * 16 * TT + e));
-        }
-      }
-      return sum;
-    };
-    if (rank == 1)
-      for (int i = threadIdx.x; i < nt * 16 * TT; i += blockDim.x)
-        cl_st_peer(base + 4u * i, 0, mine(i / (16 * TT), i % (16 * TT)));
-    cl_cluster_sync();
-    if (rank == 0) {
-      for (int i = threadIdx.x; i < nt * 16 * TT; i += blockDim.x) {
-        const float sum = mine(i / (16 * TT), i % (16 * TT)) + cl_lds(base + 4u * i);
-        const int row = (t0 + i / (16 * TT)) * 16 + (i % (16 * TT)) / TT, t = i % TT;
-        if (row < p.N && t < T) p.Y[static_cast<int64_t>(tok0 + t) * p.N + row] = __float2bfloat16_rn(sum);
-      }
-    }
-    if (t0 + PT < t_hi) cl_cluster_sync();     // both have read their sums before the next pass writes them
-  }
-}
-
 // ---- one or two tokens ---------------------------------------------------------------------------------
 // Lookups, X and the codes all pass through the SM's one shared-memory pipe, and with one token that pipe binds
 // as soon as HBM does; so the stream takes as little of it, and as few instructions, as it can. TMA brings units of
 // 8 rows x 256 bytes of codes (two windows of 256 elements, 4 blocks) and their 64 constants into two slots that
 // every warp keeps for itself (no barrier with another warp; 64 KB per SM in flight), refilled as soon as the
 // warp has read them into registers. A warp reads a window with two conflict-free 16-byte loads: lane l has chunk
-// l % 8 of row l / 8 and of that row + 4. In the MMA each quad of
-// lanes is then half a row (chunks 0..3 or 4..7: 128 elements), so the 16 rows of the A operand are 8 weight rows x
-// 2 halves h, and the 8 columns of B keep the halves and the two blocks e inside each apart: column 4 t + 2 h + e
+// l % 8 of row l / 8 and of that row + 4. In the MMA each quad of lanes is then half a row (chunks 0..3 or 4..7: 128
+// elements), so the 16 rows of the A operand are 8 weight rows x 2 halves h, and the 8 columns of B keep the halves and the two blocks e inside each apart: column 4 t + 2 h + e
 // is x of token t and half h, zero except where lane j holds block e = j / 2 (those lanes' registers stay zero:
 // they take no part in the load). Lane (g, j) with g = 2 r + h finds the sums of blocks 2 h and 2 h + 1 of row r
 // (and r + 4) and token t in its own accumulators where j = 2 t + h. A CTA owns a run of 8-row tiles, cut evenly
@@ -452,13 +274,13 @@ __global__ void __launch_bounds__(kC1Warps * 32, 1)
   }
 }
 
-// ---- 3 to 16 tokens -------------------------------------------------------------------------------------
+// ---- up to 16 tokens ------------------------------------------------------------------------------------
 // X no longer fits beside the stream, and reading its fragments once per 16 rows would cost the shared-memory
 // pipe more than the lookups do. So a warp keeps the fragments of 256 elements of all tokens in registers (64 of
 // them for 16 tokens) and runs up to 4 tiles of 16 rows past them, with their accumulators in registers too. A
-// CTA pair owns a run of row tiles; its 16 warps each have their own share of the contraction, and their sums meet
-// at the end of a pass of 4 tiles. Codes and constants of two tiles and 256 elements come by TMA into two slots
-// per warp (32 rows x 128 bytes, 128-byte swizzle; quad g takes row 2 (g % 4) + g / 4 of each 8, whose 8-byte
+// CTA owns a run of row tiles; its warps each have their own share of the contraction, and their sums meet at the
+// end of a pass of 4 tiles, while the next pass's codes are on their way. (Few tiles: a CTA pair shares one tile's
+// contraction.) Codes and constants of one or two tiles and 256 elements come by TMA into two slots per warp (32 rows x 128 bytes, 128-byte swizzle; quad g takes row 2 (g % 4) + g / 4 of each 8, whose 8-byte
 // loads then hit distinct banks). (Boxes of 16 rows x 64 or 128 bytes with 4-byte copies of the constants took
 // 51 us for 16 tokens through 8192 x 22016, 32 us of it for the stream alone.)
 constexpr int kC4Tiles = 4;
@@ -473,10 +295,10 @@ template <int NT> struct C4 {
 };
 
 // VEC: constants by TMA (K % 256 == 0), else by 4-byte copies.
-template <int NT, bool VEC>
-__global__ void __launch_bounds__(C4<NT>::WARPS * 32, 1) __cluster_dims__(2, 1, 1)
-    codebook_linear4_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmS, const __grid_constant__ ClParams p,
-                            const __grid_constant__ CodebookArg cb) {
+template <int NT, bool VEC, bool PAIR>
+__device__ __forceinline__ void codebook_linear4(const CUtensorMap& tmC, const CUtensorMap& tmS, const ClParams& p,
+                                                 const CodebookArg& cb) {
+  const int tok0 = blockIdx.y * 8 * NT, T = min(8 * NT, p.T - tok0);        // this group of tokens
   using C = C4<NT>;
   constexpr int TT = 8 * NT, WARPS = C::WARPS, ST = C::ST;
   extern __shared__ __align__(1024) uint8_t cl_smem[];
@@ -484,7 +306,7 @@ __global__ void __launch_bounds__(C4<NT>::WARPS * 32, 1) __cluster_dims__(2, 1, 
   const uint32_t table = window | kClTable;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int g = lane >> 2, j = lane & 3;
-  const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1;
+  const int rank = PAIR ? blockIdx.x & 1 : 0, worker = PAIR ? blockIdx.x >> 1 : blockIdx.x;
   if (base - window > kClBaseMax) {
     if (threadIdx.x == 0) raise_status(kStatusTimeout);
     return;
@@ -503,58 +325,70 @@ __global__ void __launch_bounds__(C4<NT>::WARPS * 32, 1) __cluster_dims__(2, 1, 
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(table + (static_cast<uint32_t>(i >> 5) << 8) + 4u * (i & 31)), "r"(v)
                  : "memory");
   }
-  cl_cluster_sync();
+  if constexpr (PAIR) cl_cluster_sync();
+  else __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");     // as in the kernel above
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __syncwarp();
   const uint32_t lanebyte = table | (4u * lane);
   const int gr = 2 * (g & 3) + (g >> 2);             // quad g's row of each 8
 
-  const int t_lo = static_cast<int>(static_cast<int64_t>(pair) * p.tiles / p.pairs);
-  const int t_hi = static_cast<int>(static_cast<int64_t>(pair + 1) * p.tiles / p.pairs);
-  const int part = rank * WARPS + warp;           // this warp's share of the blocks
+  const int t_lo = static_cast<int>(static_cast<int64_t>(worker) * p.tiles / p.workers);
+  const int t_hi = static_cast<int>(static_cast<int64_t>(worker + 1) * p.tiles / p.workers);
+  constexpr int PARTS = (PAIR ? 2 : 1) * WARPS;
+  const int part = rank * WARPS + warp;              // this warp's share of the contraction
   const int units = (p.nkb + 3) / 4;                 // of 256 elements
-  const int u_lo = part * units / (2 * WARPS), nu = (part + 1) * units / (2 * WARPS) - u_lo;
+  const int u_lo = part * units / PARTS, nu = (part + 1) * units / PARTS - u_lo;
   uint32_t in_slot = 0, slot = 0, phase = 0;
   bool ok = true;
-  for (int t0 = t_lo; t0 < t_hi; t0 += kC4Tiles) {
-    const int nt = min(kC4Tiles, t_hi - t0), groups = (nt + ST - 1) / ST, n = nu * groups;
-    int issued = 0, done = 0, fu = u_lo, fh = 0;     // what to fetch next: unit fu, tiles from ST fh
-    auto fetch = [&]() {
-      const uint32_t bar = bars + 8 * in_slot, sdst = scales + in_slot * C::SCALE_BYTES;
-      const int row = (t0 + ST * fh) * 16;
-      if constexpr (!VEC) {
+  // everything this warp streams, over all passes: pass (tiles ft0 .. + 3), unit, group of ST tiles
+  const int total = nu * ((t_hi - t_lo) / kC4Tiles * (kC4Tiles / ST) + ((t_hi - t_lo) % kC4Tiles + ST - 1) / ST);
+  int issued = 0, done = 0, ft0 = t_lo, fu = u_lo, fh = 0;
+  auto fetch = [&]() {
+    const uint32_t bar = bars + 8 * in_slot, sdst = scales + in_slot * C::SCALE_BYTES;
+    const int row = (ft0 + ST * fh) * 16;
+    if constexpr (!VEC) {
 #pragma unroll
-        for (int e = lane; e < ST * 64; e += 32) {
-          const int r = row + (e >> 2), kb = 4 * fu + (e & 3);
-          const bool in = r < p.N && kb < p.nkb;
-          c1_cp4(sdst + 4u * e, p.absmax + (in ? static_cast<int64_t>(r) * p.nkb + kb : 0), in ? 4u : 0u);
-        }
-        c1_cp_arrive(bar);
+      for (int e = lane; e < ST * 64; e += 32) {
+        const int r = row + (e >> 2), kb = 4 * fu + (e & 3);
+        const bool in = r < p.N && kb < p.nkb;
+        c1_cp4(sdst + 4u * e, p.absmax + (in ? static_cast<int64_t>(r) * p.nkb + kb : 0), in ? 4u : 0u);
       }
-      if (lane == 0) {
-        c1_expect(bar, C::CODE_BYTES + (VEC ? C::SCALE_BYTES : 0));
-        c1_tma(slots + in_slot * C::CODE_BYTES, &tmC, bar, fu * 128, row);
-        if constexpr (VEC) c1_tma(sdst, &tmS, bar, fu * 4, row);
-      }
-      in_slot ^= 1;
-      ++issued;
-      if (++fh == groups) { fh = 0; ++fu; }
-    };
-    if (n > 0) fetch();
-    if (n > 1) fetch();
+      c1_cp_arrive(bar);
+    }
+    if (lane == 0) {
+      c1_expect(bar, C::CODE_BYTES + (VEC ? C::SCALE_BYTES : 0));
+      c1_tma(slots + in_slot * C::CODE_BYTES, &tmC, bar, fu * 128, row);
+      if constexpr (VEC) c1_tma(sdst, &tmS, bar, fu * 4, row);
+    }
+    in_slot ^= 1;
+    ++issued;
+    if (ST * ++fh >= min(kC4Tiles, t_hi - ft0)) {
+      fh = 0;
+      if (++fu == u_lo + nu) { fu = u_lo; ft0 += kC4Tiles; }
+    }
+  };
+  if (total > 0) fetch();
+  if (total > 1) fetch();
+  uint4 x[4][NT][2];           // the fragments of a unit
+  for (int t0 = t_lo; t0 < t_hi; t0 += kC4Tiles) {
+    const int nt = min(kC4Tiles, t_hi - t0);
     float acc[kC4Tiles][NT][4] = {};
     for (int u = 0; u < nu && ok; ++u) {
-      uint4 x[4][NT][2];
+      if (nu > 1 || t0 == t_lo) {
 #pragma unroll
-      for (int b = 0; b < 4; ++b)
+        for (int b = 0; b < 4; ++b)
 #pragma unroll
-        for (int m = 0; m < NT; ++m) {
-          x[b][m][0] = x[b][m][1] = make_uint4(0, 0, 0, 0);
-          const int kb = 4 * (u_lo + u) + b;
-          if (8 * m + g < p.T && kb < p.nkb) {
-            const uint4* xp = reinterpret_cast<const uint4*>(p.X + (static_cast<int64_t>(8 * m + g) * p.nkb + kb) * 64 + 16 * j);
-            x[b][m][0] = __ldg(xp);
-            x[b][m][1] = __ldg(xp + 1);
+          for (int m = 0; m < NT; ++m) {
+            x[b][m][0] = x[b][m][1] = make_uint4(0, 0, 0, 0);
+            const int kb = 4 * (u_lo + u) + b;
+            if (8 * m + g < T && kb < p.nkb) {
+              const uint4* xp = reinterpret_cast<const uint4*>(p.X + (static_cast<int64_t>(tok0 + 8 * m + g) * p.nkb + kb) * 64 + 16 * j);
+              x[b][m][0] = __ldg(xp);
+              x[b][m][1] = __ldg(xp + 1);
+            }
           }
-        }
+      }
 #pragma unroll
       for (int t = 0; t < kC4Tiles; ++t) {
         if (t >= nt || !ok) break;
@@ -574,7 +408,7 @@ __global__ void __launch_bounds__(C4<NT>::WARPS * 32, 1) __cluster_dims__(2, 1, 
           slot ^= 1;
           phase ^= slot ^ 1;
           ++done;
-          if (issued < n) fetch();
+          if (issued < total) fetch();
         }
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
@@ -604,11 +438,6 @@ __global__ void __launch_bounds__(C4<NT>::WARPS * 32, 1) __cluster_dims__(2, 1, 
         }
       }
     }
-    for (; done < issued; ++done) {                  // after a wait that gave up: this warp's copies in flight
-      mbar_wait_short_addr(bars + 8 * slot, phase);
-      slot ^= 1;
-      phase ^= slot ^ 1;
-    }
 #pragma unroll
     for (int t = 0; t < kC4Tiles; ++t)
 #pragma unroll
@@ -624,18 +453,38 @@ __global__ void __launch_bounds__(C4<NT>::WARPS * 32, 1) __cluster_dims__(2, 1, 
       for (int w = 0; w < WARPS; ++w) sum += cl_lds(red + static_cast<uint32_t>(w) * C::SUM_BYTES + 4u * e);
       return sum;
     };
-    if (rank == 1)
-      for (int e = threadIdx.x; e < nt * 16 * TT; e += blockDim.x) cl_st_peer(base + 4u * e, 0, mine(e));
-    cl_cluster_sync();
+    if constexpr (PAIR) {                            // one tile: one pass
+      if (rank == 1)
+        for (int e = threadIdx.x; e < nt * 16 * TT; e += blockDim.x) cl_st_peer(base + 4u * e, 0, mine(e));
+      cl_cluster_sync();
+    }
     if (rank == 0) {
       for (int e = threadIdx.x; e < nt * 16 * TT; e += blockDim.x) {
-        const float sum = mine(e) + cl_lds(base + 4u * e);
+        float sum = mine(e);
+        if constexpr (PAIR) sum += cl_lds(base + 4u * e);
         const int row = t0 * 16 + e / TT, t = e % TT;
-        if (row < p.N && t < p.T) p.Y[static_cast<int64_t>(t) * p.N + row] = __float2bfloat16_rn(sum);
+        if (row < p.N && t < T) p.Y[static_cast<int64_t>(tok0 + t) * p.N + row] = __float2bfloat16_rn(sum);
       }
     }
-    if (t0 + kC4Tiles < t_hi) cl_cluster_sync();     // both have read their sums before the next pass writes them
+    __syncthreads();
   }
+  for (; done < issued; ++done) {                    // after a wait that gave up: this warp's copies in flight
+    mbar_wait_short_addr(bars + 8 * slot, phase);
+    slot ^= 1;
+    phase ^= slot ^ 1;
+  }
+}
+template <int NT, bool VEC>
+__global__ void __launch_bounds__(C4<NT>::WARPS * 32, 1)
+    codebook_linear4_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmS,
+                            const __grid_constant__ ClParams p, const __grid_constant__ CodebookArg cb) {
+  codebook_linear4<NT, VEC, false>(tmC, tmS, p, cb);
+}
+template <int NT, bool VEC>
+__global__ void __launch_bounds__(C4<NT>::WARPS * 32, 1) __cluster_dims__(2, 1, 1)
+    codebook_linear4_pair_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmS,
+                                 const __grid_constant__ ClParams p, const __grid_constant__ CodebookArg cb) {
+  codebook_linear4<NT, VEC, true>(tmC, tmS, p, cb);
 }
 
 }  // namespace qnf4
