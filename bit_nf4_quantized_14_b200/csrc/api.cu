@@ -1018,6 +1018,8 @@ int run_vocab_loss(const __nv_bfloat16* X, int64_t T, const __nv_bfloat16* W, in
     p.tiles_n = tiles_v;
     p.nkb = static_cast<int>(cdiv(K, kVlK));
     p.target = target + r0;
+    p.w = W;
+    p.w_pitch = static_cast<int>(K);
     p.ly = ly;
     p.stats = stats;
     p.weights = weights;

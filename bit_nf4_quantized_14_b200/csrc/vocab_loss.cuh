@@ -67,6 +67,8 @@ struct VlParams {
   int copied;                   // <0>: rows live in the packed copy (second map) when count < copied
   int cols, bn;                 // columns (words, or features of dX) and columns per tile
   int tiles_n, nkb;             // column tiles; contraction blocks of 64
+  const __nv_bfloat16* w;       // <0>: W, for prefetches, and its row pitch
+  int w_pitch;
   const int* target;            // <0>: per row
   const float* ly;              // <0>: target logits
   float2* stats;                // <0>: [half of a column tile][rows_max] (shift, sum)
@@ -144,11 +146,12 @@ __device__ __forceinline__ void vl_cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Every kernel of a call but the first is launched to start while the one before it ends: it waits here, before it
-// touches anything that kernel wrote or reads, and lets the next one be set up in turn.
+// Every kernel of a call but the first is launched to start while the one before it runs: it lets the next one be
+// set up in turn, and waits here before it touches anything that an earlier kernel of the call writes or reads. (A
+// kernel is set up only once every CTA of the one before it has started, so a waiting CTA holds nobody up.)
 __device__ __forceinline__ void vl_chain() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <bool GRAD, bool PAIR>
@@ -194,6 +197,16 @@ __device__ __forceinline__ void vl_gemm(const CUtensorMap& tmA, const CUtensorMa
   __syncthreads();
   if constexpr (PAIR) vl_cluster_sync();
   tc_fence_after();
+  if constexpr (!GRAD && !PAIR) {
+    // Up to 128 rows are bound by reading W, an input of the call that no kernel of it writes: while the kernels
+    // before this one run, the first 1.5 KB of every row of this CTA's tile come into L2.
+    const int bytes = min(p.nkb * 128, 1536) & ~15;
+    if (warp == 0 && p.w)
+      for (int r = worker * p.bn + lane; r < min(p.cols, (worker + 1) * p.bn); r += 32)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.w + static_cast<int64_t>(r) * p.w_pitch), "r"(min(bytes, p.w_pitch * 2))
+                     : "memory");
+    __syncwarp();
+  }
   vl_chain();
   asm volatile("fence.proxy.async;" ::: "memory");     // what earlier kernels stored, for this one's TMA
   const uint32_t tmem_base = *tmem_slot;
@@ -573,8 +586,10 @@ __global__ void __launch_bounds__(kVlFinishThreads) vl_finish_kernel(const float
   __shared__ float row_shift[32];
   vl_chain();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = static_cast<int>(blockIdx.x) * 32 + lane, rows = vl_rows(count, r0, rows_max);
+  const int row = static_cast<int>(blockIdx.x) * 32 + lane, n = *count, rows = max(0, min(rows_max, n - r0));
   const bool live = row < rows;
+  const int t = live ? token[r0 + row] : 0, y = live && weights ? target[r0 + row] : 0;
+  float g = live && dloss ? dloss[t] : 1.0f;
   // (shift, sum relative to exp(shift)) of this warp's tiles
   auto add = [](float2& a, float2 b) {
     if (b.x > a.x) {
@@ -597,16 +612,20 @@ __global__ void __launch_bounds__(kVlFinishThreads) vl_finish_kernel(const float
   }
   sm[warp][lane] = a;
   __syncthreads();
+  if (warp < 4) {                     // 8 warps' sums each, then those 4
+#pragma unroll
+    for (int w = 1; w < W / 4; ++w) add(a, sm[warp + 4 * w][lane]);
+    sm[warp][lane] = a;
+  }
+  __syncthreads();
   if (warp == 0) {
-    for (int w = 1; w < W; ++w) add(a, sm[w][lane]);
+    for (int w = 1; w < 4; ++w) add(a, sm[w][lane]);
     row_shift[lane] = a.x;
     if (live) {
       const float one = a.x > 0.0f ? expf(-a.x) : 1.0f;
-      const int t = token[r0 + row];
       loss[t] = a.x > 0.0f ? a.x + logf(a.y + one) : log1pf(a.y);
       if (weights) {
-        float g = dloss ? dloss[t] : 1.0f;
-        if (mean) g /= static_cast<float>(*count);
+        if (mean) g /= static_cast<float>(n);
         factor[row] = g / (a.y + one);
       }
     }
@@ -625,7 +644,7 @@ __global__ void __launch_bounds__(kVlFinishThreads) vl_finish_kernel(const float
     }
   }
   __syncthreads();
-  if (warp == 0 && live) weights[static_cast<int64_t>(row) * pitch + target[r0 + row]] = __float2bfloat16_rn(-a.y);
+  if (warp == 0 && live) weights[static_cast<int64_t>(row) * pitch + y] = __float2bfloat16_rn(-a.y);
 }
 
 // The tiles of dX that were cut: their partial sums in order. One CTA per tile and 8 of its rows.
