@@ -468,8 +468,8 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, config: RotaryConfig, positi
     """Turn the heads of q and k (fp32 or bf16; (T, heads, dim) or (B, T, heads, dim), any strides with
     contiguous features) by their tokens' positions, in one launch (qlora_rope); k may be None. positions:
     int32 or int64, (T,) or (B, T), plus `offset`; without positions token t sits at offset + t. inverse turns
-    back, which is the gradient. out: a pair of tensors like (q, k), the inputs themselves for in place.
-    Returns (q', k')."""
+    back, which is the gradient. out: a pair of tensors like (q, k), the inputs themselves for in place; no
+    element of them may belong to two tokens or heads. Returns (q', k')."""
     shape = q.shape
     nd = len(shape)
     dtype = _ROPE_TYPES.get(q.dtype)
@@ -481,6 +481,8 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, config: RotaryConfig, positi
         qo = torch.empty_like(q)
     elif qo.shape != shape or qo.dtype != q.dtype:
         raise ValueError("rotary: out must match the inputs")
+    elif k is not None and ko is not None and ko.data_ptr() == qo.data_ptr():
+        raise ValueError("rotary: q and k cannot be written to the same memory")
     sides = _rope_side(q, qo)
     if k is not None:
         ks = k.shape

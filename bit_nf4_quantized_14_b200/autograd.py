@@ -13,6 +13,7 @@ from __future__ import annotations
 import math
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import NF4Weight, RotaryConfig, linear_bwd, linear_fwd, quantize
 from . import rotary as _rotary
@@ -83,6 +84,7 @@ class RotaryFn(torch.autograd.Function):
         return _rotary(q, k, config, positions, offset)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq, dk):
         (positions,) = ctx.saved_tensors
         dq, dk = (g if g is None or g.stride(-1) == 1 else g.contiguous() for g in (dq, dk))
@@ -114,6 +116,7 @@ class VocabLossFn(torch.autograd.Function):
         return loss
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dloss):
         if not ctx.needs_input_grad[0]:
             return None, None, None, None, None
@@ -129,5 +132,8 @@ class VocabLossFn(torch.autograd.Function):
 def vocab_loss(x: torch.Tensor, head: torch.Tensor, targets: torch.Tensor, ignore_index: int = -100,
                reduction: str = "mean") -> torch.Tensor:
     """Differentiable vocabulary loss of hidden states x (..., K) with a frozen bf16 head (V x K) and targets
-    (...): the cross entropy of x head^T without its logits (see bit_nf4_quantized_14_b200.vocab_loss)."""
+    (...): the cross entropy of x head^T without its logits (see bit_nf4_quantized_14_b200.vocab_loss). x is taken
+    in bf16. A head that wants a gradient is refused: it would get none."""
+    if head.requires_grad and torch.is_grad_enabled():
+        raise ValueError("vocab_loss: the head is frozen and gets no gradient (detach it)")
     return VocabLossFn.apply(x, head, targets, ignore_index, reduction)

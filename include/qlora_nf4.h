@@ -320,9 +320,10 @@ int qlora_codebook_linear(const void* X, int64_t T, const void* codes, const flo
  * qlora_rope turns nx tensors (1 or 2: queries and keys) of element type `dtype` in one launch. Tensor i has
  * heads[i] heads of head_dim contiguous features; element (b, t, h, f) of `in` is at
  * b in_b + t in_t + h in_h + f (strides in elements, any order; likewise `out`). `out` is either exactly
- * `in` with the same strides (in place) or memory that does not overlap it.
+ * `in` with the same strides (in place) or memory that overlaps no input; no element is written twice.
  * Position of token t of row b: positions[b pos_b + t] + pos_offset (device, QLORA_I32 or QLORA_I64), or
- * pos_offset + t where positions is NULL. Angles are formed in fp64; the rest is fp32, rounded once.
+ * pos_offset + t where positions is NULL. Angles are formed in fp64 (good to 1e-6 up to |p| = 2^31); the rest is
+ * fp32, rounded once.
  * Rules: B, T, heads >= 1; rotary_dim <= head_dim <= QLORA_ROPE_MAX_HEAD; theta (host) finite.
  */
 #define QLORA_ROPE_MAX_DIM 512
@@ -357,8 +358,8 @@ int qlora_rope(const qlora_rope_tensor* x, int nx, int dtype, int64_t B, int64_t
  * A target that is neither ignore_index nor in [0, V) sets QLORA_STATUS_TARGET; its token is then treated
  * as ignored. fp32 logits and sums; the softmax weights are rounded to bf16 for the gradient's product.
  * Rules: T, V >= 1 (V < 2^30), K % 8 == 0, 8 <= K <= 2^20. `workspace` >= qlora_vocab_loss_workspace(T, V, K,
- * dX != NULL): with dX about 128 MB for the weights of one piece of the tokens (two bytes per token and word of
- * it) and 58 MB of partial sums, a copy of the piece's rows of X, and 12 bytes per token. Deterministic.
+ * dX != NULL): with dX at most 128 MB for the weights of one piece of the tokens (two bytes per token and word of
+ * it; more where 128 tokens, the smallest piece, need more), and 58 MB of partial sums, a copy of the piece's rows of X, and 12 bytes per token. Deterministic.
  */
 enum { QLORA_LOSS_NONE = 0, QLORA_LOSS_SUM = 1, QLORA_LOSS_MEAN = 2 };
 int qlora_vocab_loss_workspace(int64_t T, int64_t V, int64_t K, int gradient, size_t* bytes);

@@ -89,6 +89,25 @@ def test_zero_blocks_and_large_constants(lib):
     check(lib, tokens(4, K), codes, absmax, N, INT4)
 
 
+def test_long_rows(lib):
+    """X of two tokens past what stays in shared memory, and one token just inside and outside of it."""
+    for T, K in ((2, 24576 + 64), (1, 24576), (1, 24576 + 512), (2, 12288), (2, 12288 + 256)):
+        codes, absmax = weight(lib, 9, K, GRID, seed=K)
+        check(lib, tokens(T, K), codes, absmax, 9, GRID)
+
+
+def test_tokens_do_not_mix(lib):
+    """An infinite or NaN token leaves the others as they are."""
+    codes, absmax = weight(lib, 50, 512, INT4)
+    for T in (2, 8, 16, 40):
+        X = tokens(T, 512)
+        ref = lib.codebook_linear(X, codes, absmax, 50, INT4)
+        X[1, 7], X[1, 300] = float("inf"), float("nan")
+        got = lib.codebook_linear(X, codes, absmax, 50, INT4)
+        rest = [t for t in range(T) if t != 1]
+        assert torch.equal(got[rest], ref[rest]) and not bool(torch.isfinite(got[1]).any())
+
+
 @pytest.mark.parametrize("T", [1, 16])
 def test_decode_shape(lib, T):
     lv = [float(v) for v in lib.codebook()[0]]
@@ -99,8 +118,8 @@ def test_decode_shape(lib, T):
     assert torch.equal(a, lib.codebook_linear(tokens(T, 8192), q.codes, q.absmax, 8192, lv))   # deterministic
 
 
-def test_guards_capture_and_streams(lib):
-    N, K, T = 37, 192, 3
+@pytest.mark.parametrize("T,N,K", [(3, 37, 192), (1, 37, 192), (2, 300, 1024), (20, 300, 1024)])
+def test_guards_capture_and_streams(lib, T, N, K):
     codes, absmax = weight(lib, N, K, INT4)
     X = tokens(T, K)
     ref = lib.codebook_linear(X, codes, absmax, N, INT4)

@@ -78,6 +78,13 @@ def test_strides(lib):
     out = torch.empty(3, 9, 4, 48, device="cuda")
     check(lib, one, None, cfg, out=(out, None))
     assert lib.rotary(one[0], None, cfg)[0].equal(out[0])       # (T, heads, dim)
+    assert lib.rotary(one, None, cfg)[0].equal(out)             # an expanded input gets an output of its own
+
+
+def test_more_batch_rows_than_a_grid_takes(lib):
+    x = rand((65535 + 300, 1, 1, 4), torch.float32)
+    pos = torch.randint(0, 1000, (65835, 1), device="cuda", dtype=torch.int32)
+    check(lib, x, None, lib.RotaryConfig(4, layout="interleaved"), pos)
 
 
 def test_in_place_touches_nothing_else(lib):
@@ -151,6 +158,8 @@ def test_refusals(lib):
         lib.rotary(x, None, cfg, torch.zeros(2, dtype=torch.int64, device="cuda"))
     with pytest.raises(ValueError):
         lib.rotary(x, None, lib.RotaryConfig(32, layout="pairs"))
+    with pytest.raises(ValueError):
+        lib.rotary(x, x, cfg, out=(x, x))
     for R in (48, 31):
         with pytest.raises(lib.QLoRAError):
             lib.rotary(x, None, lib.RotaryConfig(R))

@@ -174,6 +174,12 @@ def test_autograd(lib):
     assert torch.equal(x.grad, lib.vocab_loss(X, W, y, reduction="none", dloss=g)[1])
     with torch.no_grad():
         assert vocab_loss(X, W, y).requires_grad is False
+    with pytest.raises(ValueError):
+        vocab_loss(X, W.clone().requires_grad_(), y)          # the head is frozen
+    x = X.clone().requires_grad_()
+    (dx,) = torch.autograd.grad(vocab_loss(x, W, y), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        dx.sum().backward()                                   # once differentiable
 
 
 def test_gradient_against_differences(lib):
@@ -224,6 +230,35 @@ def test_capture_streams_and_two_calls_at_once(lib):
             got.append(lib.vocab_loss(a, W, b))
     torch.cuda.synchronize()
     assert torch.equal(got[0][1], dref) and torch.equal(got[1][1], dref2) and lib.get_status() == 0
+
+
+def test_backward_captured_beside_an_eager_graph(lib):
+    """A training step captured while an eager loss of the same leaf is still alive, replayed on new inputs. (The
+    eager one is built on the capturing stream too: torch ties a leaf's gradient to the stream of its first live
+    graph, and refuses to capture, for any operator, where that is the default stream.)"""
+    from bit_nf4_quantized_14_b200.autograd import vocab_loss
+    X, W, y = case(150, 900, 64, seed=11)
+    x = X.clone().requires_grad_()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        alive = vocab_loss(x, W, y)
+        (warm,) = torch.autograd.grad(vocab_loss(x, W, y), x)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        loss = vocab_loss(x, W, y)
+        (dx,) = torch.autograd.grad(loss, x)
+    X2, _, y2 = case(150, 900, 64, seed=12)
+    with torch.no_grad():
+        x.copy_(X2)
+        y.copy_(y2)
+    graph.replay()
+    torch.cuda.synchronize()
+    ref, dref = lib.vocab_loss(X2, W, y2)
+    assert torch.equal(loss, ref) and torch.equal(dx, dref)
+    (da,) = torch.autograd.grad(alive, x)
+    assert torch.equal(da, warm)
 
 
 def test_refusals(lib):
