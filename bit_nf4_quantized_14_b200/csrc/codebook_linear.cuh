@@ -20,8 +20,8 @@
 namespace qnf4 {
 
 constexpr int kClMaxTokens = 64;
-// Measured (a weight in HBM, calls back to back): 22016 x 8192 at one token 24 us (4.2 TB/s), 4 tokens 31, 16
-// tokens 43; 8192 x 8192 at one token 12.5 us. The plain copy's rate would be 15.5 and 5.8 us.
+// Measured (a weight in HBM, calls back to back): 22016 x 8192 at one token 24 us (4.2 TB/s), 4 tokens 28, 16
+// tokens 40; 8192 x 8192 at one token 12.5 us. The plain copy's rate would be 15.5 and 5.8 us.
 //
 // Shared memory: the table (256 entries of 256 bytes, the lane copies in the first 128) sits at shared address
 // 64 KB, so one byte permute forms a lookup's address; the stream's slots lie above it, sums (and X) below.
@@ -343,14 +343,17 @@ __device__ __forceinline__ void codebook_linear4(const CUtensorMap& tmC, const C
   bool ok = true;
   // everything this warp streams, over all passes: pass (tiles ft0 .. + 3), unit, group of ST tiles
   const int total = nu * ((t_hi - t_lo) / kC4Tiles * (kC4Tiles / ST) + ((t_hi - t_lo) % kC4Tiles + ST - 1) / ST);
-  int issued = 0, done = 0, ft0 = t_lo, fu = u_lo, fh = 0;
+  // CTAs begin at different units of their warps' shares, so that they do not all ask L2 for the same lines of X at
+  // once
+  const int rot = nu > 0 ? static_cast<int>(blockIdx.x) % nu : 0;
+  int issued = 0, done = 0, ft0 = t_lo, fu = rot, fn = 0, fh = 0;
   auto fetch = [&]() {
     const uint32_t bar = bars + 8 * in_slot, sdst = scales + in_slot * C::SCALE_BYTES;
     const int row = (ft0 + ST * fh) * 16;
     if constexpr (!VEC) {
 #pragma unroll
       for (int e = lane; e < ST * 64; e += 32) {
-        const int r = row + (e >> 2), kb = 4 * fu + (e & 3);
+        const int r = row + (e >> 2), kb = 4 * (u_lo + fu) + (e & 3);
         const bool in = r < p.N && kb < p.nkb;
         c1_cp4(sdst + 4u * e, p.absmax + (in ? static_cast<int64_t>(r) * p.nkb + kb : 0), in ? 4u : 0u);
       }
@@ -358,14 +361,15 @@ __device__ __forceinline__ void codebook_linear4(const CUtensorMap& tmC, const C
     }
     if (lane == 0) {
       c1_expect(bar, C::CODE_BYTES + (VEC ? C::SCALE_BYTES : 0));
-      c1_tma(slots + in_slot * C::CODE_BYTES, &tmC, bar, fu * 128, row);
-      if constexpr (VEC) c1_tma(sdst, &tmS, bar, fu * 4, row);
+      c1_tma(slots + in_slot * C::CODE_BYTES, &tmC, bar, (u_lo + fu) * 128, row);
+      if constexpr (VEC) c1_tma(sdst, &tmS, bar, (u_lo + fu) * 4, row);
     }
     in_slot ^= 1;
     ++issued;
     if (ST * ++fh >= min(kC4Tiles, t_hi - ft0)) {
       fh = 0;
-      if (++fu == u_lo + nu) { fu = u_lo; ft0 += kC4Tiles; }
+      if (++fu == nu) fu = 0;
+      if (++fn == nu) { fn = 0; ft0 += kC4Tiles; }
     }
   };
   if (total > 0) fetch();
@@ -374,7 +378,8 @@ __device__ __forceinline__ void codebook_linear4(const CUtensorMap& tmC, const C
   for (int t0 = t_lo; t0 < t_hi; t0 += kC4Tiles) {
     const int nt = min(kC4Tiles, t_hi - t0);
     float acc[kC4Tiles][NT][4] = {};
-    for (int u = 0; u < nu && ok; ++u) {
+    for (int un = 0; un < nu && ok; ++un) {
+      const int u = un + rot < nu ? un + rot : un + rot - nu;
       if (nu > 1 || t0 == t_lo) {
 #pragma unroll
         for (int b = 0; b < 4; ++b)
