@@ -949,7 +949,7 @@ VlPlan vl_plan(int64_t T, int64_t V, int64_t K, bool grad) {
   w.packed = take(static_cast<size_t>(w.rows) * K * 2);
   w.stats = take(static_cast<size_t>(2 * cdiv(V, w.bn)) * w.rows * sizeof(float2));
   if (grad) {
-    w.factor = take(static_cast<size_t>(w.rows) * 4);
+    w.factor = take(static_cast<size_t>(w.rows) * sizeof(float2));
     w.weights = take(static_cast<size_t>(w.rows) * w.pitch * 2);
     w.part = take(static_cast<size_t>(kVlParts) * w.workers * mt * kVlN * 4);
   }
@@ -983,7 +983,7 @@ int run_vocab_loss(const __nv_bfloat16* X, int64_t T, const __nv_bfloat16* W, in
   auto* packed = reinterpret_cast<__nv_bfloat16*>(ws + L.packed);
   auto* stats = reinterpret_cast<float2*>(ws + L.stats);
   auto* weights = dX ? reinterpret_cast<__nv_bfloat16*>(ws + L.weights) : nullptr;
-  float* factor = dX ? reinterpret_cast<float*>(ws + L.factor) : nullptr;
+  auto* factor = dX ? reinterpret_cast<float2*>(ws + L.factor) : nullptr;
   const int mean = reduction == QLORA_LOSS_MEAN ? 1 : 0;
   const int rows = static_cast<int>(L.rows), mt = L.pair ? 2 * kVlM : kVlM;
   if (t64)
@@ -1027,7 +1027,7 @@ int run_vocab_loss(const __nv_bfloat16* X, int64_t T, const __nv_bfloat16* W, in
     const int64_t tiles = cdiv(here, mt) * tiles_v;
     if (int e = launch_vl_gemm<false>(L.pair, static_cast<int>(std::min<int64_t>(tiles, L.workers)), tx, tpk, tw, p, st)) return e;
     if (int e = vl_launched(launch_pdl_smem(vl_finish_kernel, dim3(static_cast<unsigned>(cdiv(here, 32))), kVlFinishThreads, 0, st, stats,
-                                            static_cast<int>(r0), here, 2 * tiles_v, L.bn / 2, count, token, target, static_cast<int>(V),
+                                            static_cast<int>(r0), here, 2 * tiles_v, L.bn / 2, count, token, static_cast<int>(V),
                                             dloss, mean, tok_loss, weights, L.pitch, factor), __LINE__))
       return e;
     if (!dX) continue;

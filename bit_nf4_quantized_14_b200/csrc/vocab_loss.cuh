@@ -17,10 +17,12 @@
 //               epilogue: exp(d_v) rounded to bf16 (the MMA operand of the gradient; a relative 2^-8 of each weight
 //               at most) and its fp32 sum over the tile's words. Where a tile's largest d exceeds 40 its weights
 //               are stored relative to that d (a shift per row and tile), so nothing overflows;
-//   vl_finish   adds the tiles' sums in order, loss, the weight -Z of the target, the row's
-//               factor g / (1 + Z); brings a row whose tiles have shifts to one shift;
+//   vl_finish   adds the tiles' sums in order, loss, the row's factor g / (1 + Z) and the target's g Z / (1 + Z);
+//               brings a row whose tiles have shifts to one shift;
 //   vl_gemm<1>  dX = weights x W (contraction over the vocabulary, W as the MN-major operand), times the row's
-//               factor in fp32, rounded once to bf16. Whole waves of tiles run in step along the vocabulary, so W
+//               factor, less the target's share of W_y, both in fp32, rounded once to bf16. (With -Z among the bf16
+//               weights its rounding alone was half of the gradient's error: 2.4e-3 against 1.7e-3 now, which is
+//               the result's own rounding.) Whole waves of tiles run in step along the vocabulary, so W
 //               and the weights pass through L2 once; the tiles of a last, partly filled wave are cut along the
 //               vocabulary to fill the CTA pairs (2048 x 4096 outputs are 128 tiles for 74 pairs) and leave fp32
 //               partial sums that vl_reduce adds in order. (One run of all tiles' steps cut evenly over the pairs
@@ -75,7 +77,7 @@ struct VlParams {
   __nv_bfloat16* weights;       // <0>: [rows][pitch], or null (loss only)
   int64_t pitch;
   const int* token;             // <1>: the token of each row
-  const float* factor;          // <1>: per row
+  const float2* factor;         // <1>: per row, of the product and of W_y
   __nv_bfloat16* out;           // <1>: [token][cols]
   float* part;                  // <1>: partial tiles of [128 CTAS][256]
 };
@@ -144,6 +146,20 @@ __device__ __forceinline__ void vl_commit(uint64_t* bar) {
 }
 __device__ __forceinline__ void vl_cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Eight features of dX: factor.x x product - factor.y x W_y (a bf16 is the upper half of its fp32); a factor of 0
+// takes nothing over from the row.
+__device__ __forceinline__ uint4 vl_dx8(const float* acc, float2 f, uint4 w) {
+  const uint32_t wv[4] = {w.x, w.y, w.z, w.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float lo = fmaf(-f.y, __uint_as_float(wv[j] << 16), acc[2 * j] * f.x);
+    const float hi = fmaf(-f.y, __uint_as_float(wv[j] & 0xffff0000u), acc[2 * j + 1] * f.x);
+    o[j] = f.x != 0.0f ? pack_bf16x2(lo, hi) : 0u;
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // Every kernel of a call but the first is launched to start while the one before it runs: it lets the next one be
@@ -312,6 +328,18 @@ __device__ __forceinline__ void vl_gemm(const CUtensorMap& tmA, const CUtensorMa
         ly = p.ly[row];
         yt = p.target[row] - t.n0;
       }
+      const bool whole = GRAD && (i < deal.full || deal.cuts == 1);
+      float2 f = make_float2(0.0f, 0.0f);
+      uint4 wy[GRAD ? 16 : 1];         // the target's row of W, this thread's half of the tile
+      if constexpr (GRAD) {
+        if (whole && live) {
+          f = p.factor[row];
+          const uint4* src = reinterpret_cast<const uint4*>(p.w + static_cast<int64_t>(p.target[row]) * p.w_pitch + t.n0 + side * hn);
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            if (8 * k < min(ncol - side * hn, hn)) wy[k] = __ldg(src + k);
+        }
+      }
       const bool ok = mbar_wait(&tfull[b], u & 1);
       if (!__all_sync(0xffffffffu, ok && !*abort_flag)) { *abort_flag = 1; break; }
       tc_fence_after();
@@ -402,13 +430,13 @@ __device__ __forceinline__ void vl_gemm(const CUtensorMap& tmA, const CUtensorMa
         release();                     // before the store below, which the arrival would wait for
         if (live) p.stats[static_cast<int64_t>(2 * (t.n0 / tn) + side) * p.rows_max + row] = make_float2(shift, sum);
       } else {
-        const bool whole = i < deal.full || deal.cuts == 1;
-        const float f = whole && live ? p.factor[row] : 0.0f;
         __nv_bfloat16* out = p.out + static_cast<int64_t>(whole && live ? p.token[row] : 0) * p.cols + t.n0;
         float* part = whole ? nullptr : p.part + (static_cast<int64_t>(i - deal.full) * kVlM * C::CTAS + in_tile) * kVlN;
         const int c_end = min(ncol, (side + 1) * hn);
-#pragma unroll 1
-        for (int c = side * hn; c < c_end; c += 16) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int c = side * hn + 16 * k;
+          if (c >= c_end) break;
           uint32_t v[16];
           tmem_ld16(taddr + c, v);
           tmem_wait_ld();
@@ -416,13 +444,7 @@ __device__ __forceinline__ void vl_gemm(const CUtensorMap& tmA, const CUtensorMa
           for (int h = 0; h < 2; ++h) {          // K % 8 == 0: whole groups of 8
             if (!live || c + 8 * h >= c_end) break;
             if (whole) {
-              uint32_t o[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float x0 = __uint_as_float(v[8 * h + 2 * j]), x1 = __uint_as_float(v[8 * h + 2 * j + 1]);
-                o[j] = f != 0.0f ? pack_bf16x2(x0 * f, x1 * f) : 0u;
-              }
-              *reinterpret_cast<uint4*>(out + c + 8 * h) = make_uint4(o[0], o[1], o[2], o[3]);
+              *reinterpret_cast<uint4*>(out + c + 8 * h) = vl_dx8(reinterpret_cast<const float*>(v + 8 * h), f, wy[2 * k + h]);
             } else {
               uint4* dst = reinterpret_cast<uint4*>(part + c + 8 * h);
               dst[0] = make_uint4(v[8 * h], v[8 * h + 1], v[8 * h + 2], v[8 * h + 3]);
@@ -578,9 +600,9 @@ __global__ void __launch_bounds__(kVlRowThreads) vl_target_kernel(const __nv_bfl
 constexpr int kVlFinishThreads = 1024;
 __global__ void __launch_bounds__(kVlFinishThreads) vl_finish_kernel(const float2* __restrict__ stats, int r0, int rows_max, int tiles,
                                                         int bn, const int* __restrict__ count, const int* __restrict__ token,
-                                                        const int* __restrict__ target, int V,
+                                                        int V,
                                                         const float* __restrict__ dloss, int mean, float* __restrict__ loss,
-                                                        __nv_bfloat16* weights, int64_t pitch, float* __restrict__ factor) {
+                                                        __nv_bfloat16* weights, int64_t pitch, float2* __restrict__ factor) {
   constexpr int W = kVlFinishThreads / 32;
   __shared__ float2 sm[W][32];
   __shared__ float row_shift[32];
@@ -588,7 +610,7 @@ __global__ void __launch_bounds__(kVlFinishThreads) vl_finish_kernel(const float
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = static_cast<int>(blockIdx.x) * 32 + lane, n = *count, rows = max(0, min(rows_max, n - r0));
   const bool live = row < rows;
-  const int t = live ? token[r0 + row] : 0, y = live && weights ? target[r0 + row] : 0;
+  const int t = live ? token[r0 + row] : 0;
   float g = live && dloss ? dloss[t] : 1.0f;
   // (shift, sum relative to exp(shift)) of this warp's tiles
   auto add = [](float2& a, float2 b) {
@@ -626,7 +648,8 @@ __global__ void __launch_bounds__(kVlFinishThreads) vl_finish_kernel(const float
       loss[t] = a.x > 0.0f ? a.x + logf(a.y + one) : log1pf(a.y);
       if (weights) {
         if (mean) g /= static_cast<float>(n);
-        factor[row] = g / (a.y + one);
+        g /= a.y + one;
+        factor[row] = make_float2(g, g * a.y);
       }
     }
   }
@@ -643,8 +666,6 @@ __global__ void __launch_bounds__(kVlFinishThreads) vl_finish_kernel(const float
       if (s != shift) w[v] = __float2bfloat16_rn(__bfloat162float(w[v]) * expf(s - shift));
     }
   }
-  __syncthreads();
-  if (warp == 0 && live) weights[static_cast<int64_t>(row) * pitch + y] = __float2bfloat16_rn(-a.y);
 }
 
 // The tiles of dX that were cut: their partial sums in order. One CTA per tile and 8 of its rows.
@@ -670,12 +691,8 @@ __global__ void __launch_bounds__(256) vl_reduce_kernel(const __grid_constant__ 
     acc[0] += a.x; acc[1] += a.y; acc[2] += a.z; acc[3] += a.w;
     acc[4] += b.x; acc[5] += b.y; acc[6] += b.z; acc[7] += b.w;
   }
-  const float f = p.factor[row];
-  uint4 o = make_uint4(0, 0, 0, 0);
-  if (f != 0.0f)
-    o = make_uint4(pack_bf16x2(acc[0] * f, acc[1] * f), pack_bf16x2(acc[2] * f, acc[3] * f),
-                   pack_bf16x2(acc[4] * f, acc[5] * f), pack_bf16x2(acc[6] * f, acc[7] * f));
-  *reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(p.token[row]) * p.cols + n0 + c) = o;
+  const uint4 w = __ldg(reinterpret_cast<const uint4*>(p.w + static_cast<int64_t>(p.target[row]) * p.w_pitch + n0 + c));
+  *reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(p.token[row]) * p.cols + n0 + c) = vl_dx8(acc, p.factor[row], w);
 }
 
 // total = sum of the tokens' losses (fp64, fixed order), over their count for a mean (0 / 0 = NaN when no

@@ -24,6 +24,9 @@ What it computes, in the pages' order (citations are to the source pages by titl
                [QLoRA explainer, prism.theerrors.in, "Putting it together";
                 PEFT page, "Paged optimizers, and QLoRA end to end"]
 
+  decoder_ops.py  64-bit forms (torch, any device; import it by name) of the operators beside the linears in a
+               decoder: rotary positions, the vocabulary loss with its gradient, the weight of a codebook
+
 Floating point is fp64 except where a step is defined as a rounding to fp32, bf16 or E4M3; those
 roundings are written out explicitly so that the CUDA path can be compared bit for bit.
 Every choice the pages leave open is named where it is made ("Reading: ...").
