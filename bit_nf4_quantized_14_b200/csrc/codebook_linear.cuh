@@ -7,7 +7,10 @@
 // a 256-entry table, one copy per lane so the lookups have no bank conflicts. Inside a block of 64 the MMA's k
 // index is permuted alike on both operands, so lane j of a quad holds elements 16 j .. 16 j + 15: 8 code bytes and
 // 32 bytes of X in a row. The block's constant multiplies the fp32 result of its four MMAs, so the only rounding
-// of a weight is its level's to bf16 (a relative 2^-8 at most), as in the T <= 16 forward of the double-quantized layer.
+// of a weight is its level's to bf16 (a relative 2^-8 at most). The host picks a common factor for the levels under
+// which they round best (int4's sevenths become exact), and the fp32 sums are divided by it at the end. Distance from
+// the 64-bit result (2-norm), of which the rounding of the result alone is 1.6e-3: NF4 at 8192 x 8192 1.9e-3 (2.1e-3
+// with the levels as they are), int4 with 16 tokens 1.7e-3 (2.3e-3).
 // Two kernels: one for one or two tokens, one for up to 16 (more run as groups of 16, whose weights after the first
 // come from L2 where they fit). In both every warp streams its own share of a CTA's rows or contraction with no
 // barrier between warps, and fp32 sums are added in a fixed order: deterministic.
@@ -33,6 +36,7 @@ struct ClParams {
   const __nv_bfloat16* X;
   const uint8_t* codes;
   const float* absmax;
+  float unscale;                         // the table holds levels / unscale
   __nv_bfloat16* Y;
 };
 
@@ -62,8 +66,8 @@ __device__ __forceinline__ void cl_sts2(uint32_t addr, float a, float b) {
 // every warp keeps for itself (no barrier with another warp; 64 KB per SM in flight), refilled as soon as the
 // warp has read them into registers. A warp reads a window with two conflict-free 16-byte loads: lane l has chunk
 // l % 8 of row l / 8 and of that row + 4. In the MMA each quad of lanes is then half a row (chunks 0..3 or 4..7: 128
-// elements), so the 16 rows of the A operand are 8 weight rows x 2 halves h, and the 8 columns of B keep the halves and the two blocks e inside each apart: column 4 t + 2 h + e
-// is x of token t and half h, zero except where lane j holds block e = j / 2 (those lanes' registers stay zero:
+// elements), so the 16 rows of the A operand are 8 weight rows x 2 halves h, and the 8 columns of B keep the halves
+// and the two blocks e inside each apart: column 4 t + 2 h + e is x of token t and half h, zero except where lane j holds block e = j / 2 (those lanes' registers stay zero:
 // they take no part in the load). Lane (g, j) with g = 2 r + h finds the sums of blocks 2 h and 2 h + 1 of row r
 // (and r + 4) and token t in its own accumulators where j = 2 t + h. A CTA owns a run of 8-row tiles, cut evenly
 // over its warps. (Loads into registers 4 windows ahead took 39 us for 22016 x 8192: the lookups' waits shared
@@ -268,7 +272,7 @@ __global__ void __launch_bounds__(kC1Warps * 32, 1)
         sum += cl_lds(red) + cl_lds(red + 8u);
       }
       const int out = (t0 + tile) * 8 + r;
-      if (out < p.N) p.Y[static_cast<int64_t>(t) * p.N + out] = __float2bfloat16_rn(sum);
+      if (out < p.N) p.Y[static_cast<int64_t>(t) * p.N + out] = __float2bfloat16_rn(sum * p.unscale);
     }
     __syncthreads();
   }
@@ -280,7 +284,8 @@ __global__ void __launch_bounds__(kC1Warps * 32, 1)
 // them for 16 tokens) and runs up to 4 tiles of 16 rows past them, with their accumulators in registers too. A
 // CTA owns a run of row tiles; its warps each have their own share of the contraction, and their sums meet at the
 // end of a pass of 4 tiles, while the next pass's codes are on their way. (Few tiles: a CTA pair shares one tile's
-// contraction.) Codes and constants of one or two tiles and 256 elements come by TMA into two slots per warp (32 rows x 128 bytes, 128-byte swizzle; quad g takes row 2 (g % 4) + g / 4 of each 8, whose 8-byte
+// contraction.) Codes and constants of one or two tiles and 256 elements come by TMA into two slots per warp
+// (32 rows x 128 bytes, 128-byte swizzle; quad g takes row 2 (g % 4) + g / 4 of each 8, whose 8-byte
 // loads then hit distinct banks). (Boxes of 16 rows x 64 or 128 bytes with 4-byte copies of the constants took
 // 51 us for 16 tokens through 8192 x 22016, 32 us of it for the stream alone.)
 constexpr int kC4Tiles = 4;
@@ -468,7 +473,7 @@ __device__ __forceinline__ void codebook_linear4(const CUtensorMap& tmC, const C
         float sum = mine(e);
         if constexpr (PAIR) sum += cl_lds(base + 4u * e);
         const int row = t0 * 16 + e / TT, t = e % TT;
-        if (row < p.N && t < T) p.Y[static_cast<int64_t>(tok0 + t) * p.N + row] = __float2bfloat16_rn(sum);
+        if (row < p.N && t < T) p.Y[static_cast<int64_t>(tok0 + t) * p.N + row] = __float2bfloat16_rn(sum * p.unscale);
       }
     }
     __syncthreads();
