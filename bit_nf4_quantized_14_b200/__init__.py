@@ -559,6 +559,8 @@ def vocab_loss(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, ignore_i
         if dXo.shape != X.shape:
             raise ValueError("vocab_loss: dX must be like X")
     _same_device(dev, W=W, targets=targets, dloss=dloss, dX=dXo, workspace=workspace)
+    if workspace is not None:
+        _need(workspace, workspace.dtype, "workspace")      # numel of a broadcast one says more than it holds
     V = W.shape[0]
     ws = workspace if workspace is not None else torch.empty(vocab_loss_workspace_bytes(T, V, K, dXo is not None),
                                                              dtype=torch.uint8, device=X.device)

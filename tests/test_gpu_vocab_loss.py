@@ -277,3 +277,13 @@ def test_refusals(lib):
     with pytest.raises(lib.QLoRAError) as e:
         lib.vocab_loss(X[:, :60].contiguous(), W[:, :60].contiguous(), y)
     assert e.value.code == -2
+
+
+def test_broadcast_workspace_is_refused(lib):
+    """Its numel is that of a real workspace, its memory one byte (refused on the host, before any launch)."""
+    X = torch.zeros(4, 64, dtype=torch.bfloat16, device="cuda")
+    W = torch.zeros(10, 64, dtype=torch.bfloat16, device="cuda")
+    need = lib.vocab_loss_workspace_bytes(4, 10, 64, True)
+    one = torch.empty(1, dtype=torch.uint8, device="cuda")
+    with pytest.raises(ValueError, match="workspace"):
+        lib.vocab_loss(X, W, torch.zeros(4, dtype=torch.int64, device="cuda"), workspace=one.expand(need))
