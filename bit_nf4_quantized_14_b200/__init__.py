@@ -152,6 +152,14 @@ def _on(device: int):
     return _HERE_ALREADY if device == torch._C._cuda_getDevice() else torch.cuda.device(device)
 
 
+def _given(stream, t: torch.Tensor):
+    """The stream of a call made current: what the call allocates for itself and for its results then belongs to it,
+    so no other stream is given that memory, or still works on it, while this one does."""
+    if stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+    return torch.cuda.stream(stream)
+
+
 def _same_device(device: int, **tensors) -> None:
     for name, t in tensors.items():
         if t is not None and t.get_device() != device:
@@ -378,6 +386,9 @@ def codebook_linear(X: torch.Tensor, codes: torch.Tensor, absmax: torch.Tensor, 
                     out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Y = X W^T (T x N bf16) for X (T x K bf16, T <= CODEBOOK_LINEAR_MAX_TOKENS) and the N x K weight that
     codebook_quantize(w, levels) wrote as codes and absmax (qlora_codebook_linear). K % 64 == 0."""
+    if stream is not None:
+        with _given(stream, X):
+            return codebook_linear(X, codes, absmax, N, levels, out)
     if X.dim() != 2:
         raise ValueError("codebook_linear: X must be T x K")
     _need(X, torch.bfloat16, "X")
@@ -397,7 +408,7 @@ def codebook_linear(X: torch.Tensor, codes: torch.Tensor, absmax: torch.Tensor, 
     lv, nl = _level_array(tuple(levels))
     with _on(dev):
         _check(load().qlora_codebook_linear(X.data_ptr(), T, codes.data_ptr(), absmax.data_ptr(), N, K, lv, nl,
-                                            out.data_ptr(), _stream(stream)), "qlora_codebook_linear")
+                                            out.data_ptr(), _stream(None)), "qlora_codebook_linear")
     return out
 
 
@@ -470,6 +481,9 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, config: RotaryConfig, positi
     int32 or int64, (T,) or (B, T), plus `offset`; without positions token t sits at offset + t. inverse turns
     back, which is the gradient. out: a pair of tensors like (q, k), the inputs themselves for in place; no
     element of them may belong to two tokens or heads. Returns (q', k')."""
+    if stream is not None:
+        with _given(stream, q):
+            return rotary(q, k, config, positions, offset, inverse, out)
     shape = q.shape
     nd = len(shape)
     dtype = _ROPE_TYPES.get(q.dtype)
@@ -511,7 +525,7 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, config: RotaryConfig, positi
         pos_b = pst[0] if len(ps) == 2 else 0
     with _on(dev):
         _check(load().qlora_rope(sides, 1 if k is None else 2, dtype, B, T, shape[-1], config.rotary_dim, layout, th, mscale,
-                                 pos, pos_type, pos_b, offset, 1 if inverse else 0, _stream(stream)), "qlora_rope")
+                                 pos, pos_type, pos_b, offset, 1 if inverse else 0, _stream(None)), "qlora_rope")
     return qo, ko
 
 
@@ -534,6 +548,9 @@ def vocab_loss(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, ignore_i
     without keeping the logits, and its gradient with respect to X (qlora_vocab_loss). reduction: "mean" over
     the tokens whose target is not ignore_index, "sum", or "none" (a loss per token, whose gradients `dloss`,
     fp32, default to ones). Returns (loss fp32, dX bf16 or None); W is frozen and gets no gradient."""
+    if stream is not None:
+        with _given(stream, X):
+            return vocab_loss(X, W, targets, ignore_index, reduction, dloss, need_dx, dX, workspace)
     if reduction not in LOSS_REDUCTIONS:
         raise ValueError(f"vocab_loss: unknown reduction {reduction!r}")
     if dloss is not None and reduction != "none":
@@ -571,7 +588,7 @@ def vocab_loss(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, ignore_i
         _check(load().qlora_vocab_loss(X.data_ptr(), T, W.data_ptr(), V, K, targets.data_ptr(),
                                        QLORA_I32 if targets.dtype == torch.int32 else QLORA_I64, ignore_index, red,
                                        _ptr(dloss), None if red else at, at if red else None, _ptr(dXo), ws.data_ptr(),
-                                       ws.numel(), _stream(stream)), "qlora_vocab_loss")
+                                       ws.numel(), _stream(None)), "qlora_vocab_loss")
     return loss, dXo
 
 

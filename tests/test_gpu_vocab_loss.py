@@ -8,6 +8,8 @@ itself. The gradient: each weight p_v is off by that relatively and by half a bf
 words by (V/16 + 16) 2^-23 of sum p |W|, the result by half a bf16 step. fp32 and bf16 end at 2^-126: a weight
 below it may be lost whole, so V words can lose V 2^-126 of the loss and V 2^-126 max |W| of a gradient.
 """
+import math
+
 import pytest
 import torch
 
@@ -287,3 +289,25 @@ def test_broadcast_workspace_is_refused(lib):
     one = torch.empty(1, dtype=torch.uint8, device="cuda")
     with pytest.raises(ValueError, match="workspace"):
         lib.vocab_loss(X, W, torch.zeros(4, dtype=torch.int64, device="cuda"), workspace=one.expand(need))
+
+
+def test_memory_of_a_call_on_a_given_stream_is_the_streams(lib, monkeypatch):
+    """Every tensor that the operators make for themselves is allocated with the stream of the call current."""
+    side = torch.cuda.Stream()
+    X, W, tg, codes, absmax = (torch.zeros(*s, dtype=t, device="cuda") for s, t in (
+        ((4, 64), torch.bfloat16), ((10, 64), torch.bfloat16), ((4,), torch.int64), ((320,), torch.uint8),
+        ((10,), torch.float32)))
+    torch.cuda.synchronize()
+    seen = []
+    for name in ("empty", "empty_like"):
+        make = getattr(torch, name)
+        monkeypatch.setattr(torch, name, lambda *a, make=make, **k: (
+            seen.append(torch.cuda.current_stream().cuda_stream), make(*a, **k))[1])
+    loss, dX = lib.vocab_loss(X, W, tg, stream=side)
+    q, _ = lib.rotary(X.view(4, 1, 64), None, lib.RotaryConfig(64), stream=side)
+    Y = lib.codebook_linear(X, codes, absmax, 10, lib.codebook()[0], stream=side)
+    monkeypatch.undo()
+    side.synchronize()
+    assert len(seen) == 5 and set(seen) == {side.cuda_stream}        # dX, workspace, loss; q'; Y
+    assert abs(float(loss) - math.log(10.0)) < 1e-5                  # ten equal logits; fp32: 2.3 * 2^-24 a rounding
+    assert not dX.any() and not q.any() and not Y.any()
