@@ -9,8 +9,8 @@
 // 32 bytes of X in a row. The block's constant multiplies the fp32 result of its four MMAs, so the only rounding
 // of a weight is its level's to bf16 (a relative 2^-8 at most). The host picks a common factor for the levels under
 // which they round best (int4's sevenths become exact), and the fp32 sums are divided by it at the end. Distance from
-// the 64-bit result (2-norm), of which the rounding of the result alone is 1.6e-3: NF4 at 8192 x 8192 1.9e-3 to 2.0e-3 (2.1e-3
-// with the levels as they are), int4 with 16 tokens 1.7e-3 (2.3e-3).
+// the 64-bit result (2-norm), of which the rounding of the result alone is 1.6e-3: NF4 at 8192 x 8192 1.9e-3 to
+// 2.0e-3 (2.1e-3 with the levels as they are), int4 with 16 tokens 1.7e-3 (2.3e-3).
 // Two kernels: one for one or two tokens, one for up to 16 (more run as groups of 16, whose weights after the first
 // come from L2 where they fit). In both every warp streams its own share of a CTA's rows or contraction with no
 // barrier between warps, and fp32 sums are added in a fixed order: deterministic.
