@@ -166,6 +166,12 @@ def _same_device(device: int, **tensors) -> None:
             raise ValueError(f"{name}: expected a tensor on cuda:{device}, got {t.device}")
 
 
+def _aligned(t: torch.Tensor | None):
+    """t, or a contiguous copy of it where its memory does not begin on 16 bytes, as the library asks of every pointer:
+    a view like ids[1:], or a gradient that is a part of a larger one."""
+    return t if t is None or t.data_ptr() % 16 == 0 else t.clone(memory_format=torch.contiguous_format)
+
+
 # ---- host-only queries --------------------------------------------------------------------------
 
 def codebook():
@@ -547,7 +553,8 @@ def vocab_loss(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, ignore_i
     """Softmax cross entropy of the logits X W^T (X: T x K bf16, W: V x K bf16) with targets (T, int32 or int64),
     without keeping the logits, and its gradient with respect to X (qlora_vocab_loss). reduction: "mean" over
     the tokens whose target is not ignore_index, "sum", or "none" (a loss per token, whose gradients `dloss`,
-    fp32, default to ones). Returns (loss fp32, dX bf16 or None); W is frozen and gets no gradient."""
+    fp32, default to ones). targets and dloss may begin anywhere (ids[1:], copied where that is not on 16 bytes), X, W,
+    dX and workspace on 16 bytes. Returns (loss fp32, dX bf16 or None); W is frozen and gets no gradient."""
     if stream is not None:
         with _given(stream, X):
             return vocab_loss(X, W, targets, ignore_index, reduction, dloss, need_dx, dX, workspace)
@@ -578,6 +585,7 @@ def vocab_loss(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, ignore_i
     _same_device(dev, W=W, targets=targets, dloss=dloss, dX=dXo, workspace=workspace)
     if workspace is not None:
         _need(workspace, workspace.dtype, "workspace")      # numel of a broadcast one says more than it holds
+    targets, dloss = _aligned(targets), _aligned(dloss)
     V = W.shape[0]
     ws = workspace if workspace is not None else torch.empty(vocab_loss_workspace_bytes(T, V, K, dXo is not None),
                                                              dtype=torch.uint8, device=X.device)

@@ -311,3 +311,37 @@ def test_memory_of_a_call_on_a_given_stream_is_the_streams(lib, monkeypatch):
     assert len(seen) == 5 and set(seen) == {side.cuda_stream}        # dX, workspace, loss; q'; Y
     assert abs(float(loss) - math.log(10.0)) < 1e-5                  # ten equal logits; fp32: 2.3 * 2^-24 a rounding
     assert not dX.any() and not q.any() and not Y.any()
+
+
+@pytest.mark.parametrize("dtype", [torch.int64, torch.int32])
+@pytest.mark.parametrize("first", [1, 2, 3, 5])
+def test_targets_and_token_gradients_that_begin_anywhere(lib, dtype, first):
+    """The next-token shift of one sequence: ids[first:] begins 4 to 40 bytes into its memory. Its copy gives the
+    reference, bit for bit."""
+    from bit_nf4_quantized_14_b200.autograd import vocab_loss
+    X, W, y = case(60, 300, 64, seed=13)
+    ids = torch.cat([torch.zeros(first, dtype=torch.int64, device="cuda"), y]).to(dtype)
+    ids[first + 3] = -100
+    view, copy = ids[first:], ids[first:].clone()
+    g = torch.rand(60 + first, device="cuda")
+    for red, d, d0 in (("mean", None, None), ("none", g[first:], g[first:].clone())):
+        got, ref = (lib.vocab_loss(X, W, t, reduction=red, dloss=w) for t, w in ((view, d), (copy, d0)))
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1]) and lib.get_status() == 0
+    x, x0 = (X.clone().requires_grad_() for _ in range(2))
+    for red in ("mean", "none"):
+        for a, t in ((x, view), (x0, copy)):
+            vocab_loss(a.view(1, 60, 64), W, t.view(1, 60), reduction=red).sum().backward()
+        assert torch.equal(x.grad, x0.grad)
+
+
+def test_token_losses_of_joined_parts(lib):
+    """Per-token losses joined by torch.cat: the second part's gradient is a view that begins 7 floats in."""
+    from bit_nf4_quantized_14_b200.autograd import vocab_loss
+    X, W, y = case(18, 300, 64, seed=14)
+    w = torch.rand(18, device="cuda")
+    x = X.clone().requires_grad_()
+    parts = [vocab_loss(x[a:b], W, y[a:b], reduction="none") for a, b in ((0, 7), (7, 18))]
+    (torch.cat(parts) * w).sum().backward()
+    for a, b in ((0, 7), (7, 18)):
+        ref = lib.vocab_loss(X[a:b].clone(), W, y[a:b].clone(), reduction="none", dloss=w[a:b].clone())[1]
+        assert torch.equal(x.grad[a:b], ref)
