@@ -483,10 +483,10 @@ def _rope_side(x: torch.Tensor, o: torch.Tensor) -> bytes:
 def rotary(q: torch.Tensor, k: torch.Tensor | None, config: RotaryConfig, positions: torch.Tensor | None = None,
            offset: int = 0, inverse: bool = False, out=None, stream=None):
     """Turn the heads of q and k (fp32 or bf16; (T, heads, dim) or (B, T, heads, dim), any strides with
-    contiguous features) by their tokens' positions, in one launch (qlora_rope); k may be None. positions:
-    int32 or int64, (T,) or (B, T), plus `offset`; without positions token t sits at offset + t. inverse turns
-    back, which is the gradient. out: a pair of tensors like (q, k), the inputs themselves for in place; no
-    element of them may belong to two tokens or heads. Returns (q', k')."""
+    contiguous features, memory that begins on 16 bytes) by their tokens' positions, in one launch (qlora_rope); k may
+    be None. positions: int32 or int64, (T,) or (B, T), plus `offset`; without positions token t sits at offset + t.
+    inverse turns back, which is the gradient. out: a pair of tensors like (q, k), the inputs themselves for in
+    place; no element of them may belong to two tokens or heads. Returns (q', k')."""
     if stream is not None:
         with _given(stream, q):
             return rotary(q, k, config, positions, offset, inverse, out)

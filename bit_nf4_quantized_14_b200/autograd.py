@@ -15,7 +15,7 @@ import math
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import NF4Weight, RotaryConfig, linear_bwd, linear_fwd, quantize
+from . import NF4Weight, RotaryConfig, _aligned, linear_bwd, linear_fwd, quantize
 from . import rotary as _rotary
 from . import vocab_loss as _vocab_loss
 
@@ -81,20 +81,21 @@ class RotaryFn(torch.autograd.Function):
     def forward(ctx, q: torch.Tensor, k: torch.Tensor | None, config: RotaryConfig, positions, offset: int):
         ctx.save_for_backward(positions)
         ctx.config, ctx.offset = config, offset
-        return _rotary(q, k, config, positions, offset)
+        return _rotary(_aligned(q), _aligned(k), config, positions, offset)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dq, dk):
         (positions,) = ctx.saved_tensors
-        dq, dk = (g if g is None or g.stride(-1) == 1 else g.contiguous() for g in (dq, dk))
+        dq, dk = (_aligned(g if g is None or g.stride(-1) == 1 else g.contiguous()) for g in (dq, dk))
         dq, dk = _rotary(dq, dk, ctx.config, positions, ctx.offset, inverse=True)
         return dq, dk, None, None, None
 
 
 def rotary(q: torch.Tensor, k: torch.Tensor | None, config: RotaryConfig, positions: torch.Tensor | None = None,
            offset: int = 0):
-    """Differentiable rotary positions (see bit_nf4_quantized_14_b200.rotary): returns (q', k')."""
+    """Differentiable rotary positions (see bit_nf4_quantized_14_b200.rotary): returns (q', k'). Heads, or gradients,
+    that do not begin on 16 bytes (a part of a head behind an odd prefix) are copied first."""
     return RotaryFn.apply(q, k, config, positions, offset)
 
 

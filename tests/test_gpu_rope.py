@@ -169,3 +169,27 @@ def test_refusals(lib):
     with pytest.raises(lib.QLoRAError) as e:
         lib.rotary(rand((1, 1, 1, 40), torch.bfloat16)[..., 1:33], None, cfg)
     assert e.value.code == -3
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("prefix", [1, 4, 7, 36])
+def test_gradients_that_begin_anywhere(lib, dtype, prefix):
+    """A rotated part joined behind other features of its head, for one token (whose gradient is a contiguous view
+    `prefix` features in) and for several, and behind other heads; heads that are such a part themselves. Copies give
+    the reference, bit for bit."""
+    from bit_nf4_quantized_14_b200.autograd import rotary
+    cfg = lib.RotaryConfig(16)
+    for T, H in ((1, 1), (5, 3)):
+        whole = rand((T, H, prefix + 24), dtype).requires_grad_()
+        w = rand((T, H, prefix + 24), dtype, 1)
+        turned, none = rotary(whole[..., prefix:], None, cfg, offset=3)
+        assert none is None and torch.equal(turned, lib.rotary(whole[..., prefix:].detach().clone(), None, cfg, offset=3)[0])
+        torch.cat([whole[..., :prefix], turned], -1).backward(w)
+        ref = lib.rotary(w[..., prefix:].clone(), None, cfg, offset=3, inverse=True)[0]
+        assert torch.equal(whole.grad[..., prefix:], ref) and torch.equal(whole.grad[..., :prefix], w[..., :prefix])
+    q, k = rand((4, 3, 17), dtype).requires_grad_(), rand((4, prefix, 17), dtype, 1).requires_grad_()
+    qo, ko = rotary(q, k, cfg)
+    w = rand((4, prefix + 3, 17), dtype, 2)
+    torch.cat([ko, qo], 1).backward(w)
+    assert torch.equal(q.grad, lib.rotary(w[:, prefix:].clone(), None, cfg, inverse=True)[0])
+    assert torch.equal(k.grad, lib.rotary(w[:, :prefix].clone(), None, cfg, inverse=True)[0])
