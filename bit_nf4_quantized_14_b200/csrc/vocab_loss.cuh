@@ -13,8 +13,8 @@
 //               K = 8192 a logit of 12 came out 1e-4 low), one CTA per row; copies the rows together where
 //               tokens are left out, and zeroes those tokens' gradients;
 //   vl_gemm<0>  logits tile by tile on the tensor cores (a CTA pair: 256 rows x up to 256 words, K in steps of 64
-//               through a TMA-filled ring, two accumulators in tensor memory so the epilogue overlaps the next tile);
-//               epilogue: exp(d_v) rounded to bf16 (the MMA operand of the gradient; a relative 2^-8 of each weight
+//               through a TMA-filled ring, two accumulators in tensor memory so the epilogue overlaps the next run);
+//               epilogue: the fp32 sum of the tile's runs over K; exp(d_v) rounded to bf16 (the MMA operand of the gradient; a relative 2^-8 of each weight
 //               at most) and its fp32 sum over the tile's words. Where a tile's largest d exceeds 40 its weights
 //               are stored relative to that d (a shift per row and tile), so nothing overflows;
 //   vl_finish   adds the tiles' sums in order, loss, the row's factor g / (1 + Z) and the target's g Z / (1 + Z);
@@ -55,11 +55,12 @@ template <bool PAIR> struct VlCfg {
   static_assert(SMEM_BYTES <= 227 * 1024 && (2 * STAGES + 5) * 8 + 8 <= 256, "shared memory per CTA");
 };
 constexpr int kVlThreads = 10 * 32;       // TMA, MMA, 8 epilogue warps
-// The tensor cores drop what does not fit an accumulator's 24 bits. That loses half of the last bit per step on
-// average, always towards zero: over steps of 16 elements a logit comes out short by a share of itself that was
-// measured as 1.5e-8 to 1.9e-8 per step (K = 1024 to 8192, logits of 2 to 20; 8e-6 at K = 8192). Putting the mean
-// share back costs nothing in the epilogue's subtraction and takes the mean loss from 4e-6 to 5e-7 of the exact one.
-constexpr float kVlShort = 1.65e-8f;
+// The tensor cores drop what does not fit an accumulator's 24 bits, towards zero: in one run over K a logit loses a share of
+// itself that grows with K and depends on the data (K = 8192, relative: features of random signs 8e-6, of one sign
+// 3.4e-5, one large feature first 1.5e-5, last 0; of one sign at K = 2^20 6.7e-3). So a logit is the fp32 sum of near-equal
+// runs of at most 16 blocks (64 steps): 1e-6, of one sign 2e-6, at any K. It costs 1 to 4 % of a call (8 blocks: half the
+// error, 4 to 8 %).
+constexpr int kVlRun = 16;
 constexpr float kVlMaxShift = 40.0f;      // exp(40) x any vocabulary stays far inside fp32 and bf16
 constexpr unsigned kStatusTarget = 4u;
 
@@ -148,6 +149,15 @@ __device__ __forceinline__ void vl_cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// 16 columns of this warp's lanes of tensor memory, written.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]), "f"(v[10]),
+      "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+      : "memory");
+}
+
 // Eight features of dX: factor.x x product - factor.y x W_y (a bf16 is the upper half of its fp32); a factor of 0
 // takes nothing over from the row.
 __device__ __forceinline__ uint4 vl_dx8(const float* acc, float2 f, uint4 w) {
@@ -189,7 +199,7 @@ __device__ __forceinline__ void vl_gemm(const CUtensorMap& tmA, const CUtensorMa
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = PAIR ? blockIdx.x & 1 : 0;
   const int worker = PAIR ? blockIdx.x >> 1 : blockIdx.x, workers = PAIR ? gridDim.x >> 1 : gridDim.x;
   if (threadIdx.x == 0) {
@@ -235,6 +245,9 @@ __device__ __forceinline__ void vl_gemm(const CUtensorMap& tmA, const CUtensorMa
   const VlDeal deal = GRAD ? vl_deal(tiles, workers, p.nkb) : VlDeal{tiles, 0, 1};
   const int num_items = deal.full + deal.rest * deal.cuts;
   const int bn_cta = p.bn / C::CTAS;
+  // accumulator fills per item: the runs of a logit, near-equal ones; run r begins at block run_at(r)
+  const int runs = GRAD ? 1 : (p.nkb + kVlRun - 1) / kVlRun;
+  auto run_at = [&](int r) { return static_cast<int>(static_cast<int64_t>(p.nkb) * r / runs); };
   struct Item { int m0, n0, kb0, kb1; };
   auto item = [&](int i) {
     Item t;
@@ -252,6 +265,8 @@ __device__ __forceinline__ void vl_gemm(const CUtensorMap& tmA, const CUtensorMa
     return t;
   };
 
+  // A logits thread holds 128 sums: registers move from the first warpgroup to the epilogue's two. The launch has 168 a
+  // thread, 3 x 168 = 504 per lane of the three; the split takes 64 + 2 x 216 = 496 of them.
   if (warp == 0) {
     // ------------------------------- TMA producer (both CTAs) -------------------------------
     if (lane == 0) {
@@ -284,28 +299,30 @@ __device__ __forceinline__ void vl_gemm(const CUtensorMap& tmA, const CUtensorMa
     if (lane == 0 && rank == 0) {
       int it = 0, lt = 0;
       bool ok = true;
-      for (int i = worker; i < num_items && ok; i += workers, ++lt) {
+      for (int i = worker; i < num_items && ok; i += workers) {
         const Item t = item(i);
-        const int b = lt & 1, u = lt >> 1;
-        if (lt >= 2 && !mbar_wait(&tempty[b], (u - 1) & 1)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t d = tmem_base + static_cast<uint32_t>(b * kVlN);
-        for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
-          const int s = it % ST;
-          if (!mbar_wait(&full[s], (it / ST) & 1) || *abort_flag) { ok = false; break; }
+        for (int r = 0; r < runs && ok; ++r, ++lt) {
+          const int b = lt & 1, u = lt >> 1;
+          if (lt >= 2 && !mbar_wait(&tempty[b], (u - 1) & 1)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t a_addr = smem_u32(sA + s * kVlABytes), b_addr = smem_u32(sB + s * C::B_BYTES);
+          const uint32_t d = tmem_base + static_cast<uint32_t>(b * kVlN);
+          const int first = GRAD ? t.kb0 : run_at(r), last = GRAD ? t.kb1 : run_at(r + 1);
+          for (int kb = first; kb < last; ++kb, ++it) {
+            const int s = it % ST;
+            if (!mbar_wait(&full[s], (it / ST) & 1) || *abort_flag) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t a_addr = smem_u32(sA + s * kVlABytes), b_addr = smem_u32(sB + s * C::B_BYTES);
 #pragma unroll
-          for (int k = 0; k < kVlK / 16; ++k) {
-            const uint64_t ad = sdesc_sw128(a_addr + 32u * k, 16u, 1024u);
-            const uint64_t bd = GRAD ? sdesc_sw128(b_addr + 2048u * k, 8192u, 1024u)
-                                     : sdesc_sw128(b_addr + 32u * k, 16u, 1024u);
-            vl_mma<PAIR>(d, ad, bd, idesc, (kb > t.kb0 || k > 0) ? 1u : 0u);
+            for (int k = 0; k < kVlK / 16; ++k) {
+              const uint64_t ad = sdesc_sw128(a_addr + 32u * k, 16u, 1024u);
+              const uint64_t bd = GRAD ? sdesc_sw128(b_addr + 2048u * k, 8192u, 1024u)
+                                       : sdesc_sw128(b_addr + 32u * k, 16u, 1024u);
+              vl_mma<PAIR>(d, ad, bd, idesc, (kb > first || k > 0) ? 1u : 0u);
+            }
+            vl_commit<PAIR>(&empty[s]);
           }
-          vl_commit<PAIR>(&empty[s]);
+          if (ok) vl_commit<PAIR>(&tfull[b]);
         }
-        if (!ok) break;
-        vl_commit<PAIR>(&tfull[b]);
       }
       if (!ok) *abort_flag = 1;
       vl_commit<PAIR>(drain);
@@ -316,9 +333,8 @@ __device__ __forceinline__ void vl_gemm(const CUtensorMap& tmA, const CUtensorMa
     const uint32_t out_buf = smem_u32(sE + (warp - 2) * kVlStore);
     const int tn = p.bn;
     int lt = 0;
-    for (int i = worker; i < num_items; i += workers, ++lt) {
+    for (int i = worker; i < num_items; i += workers) {
       const Item t = item(i);
-      const int b = lt & 1, u = lt >> 1;
       const int in_tile = rank * kVlM + 32 * q + lane, row = t.m0 + in_tile;
       const bool live = row < rows;
       const int ncol = min(tn, p.cols - t.n0);
@@ -340,11 +356,18 @@ __device__ __forceinline__ void vl_gemm(const CUtensorMap& tmA, const CUtensorMa
             if (8 * k < min(ncol - side * hn, hn)) wy[k] = __ldg(src + k);
         }
       }
-      const bool ok = mbar_wait(&tfull[b], u & 1);
-      if (!__all_sync(0xffffffffu, ok && !*abort_flag)) { *abort_flag = 1; break; }
-      tc_fence_after();
-      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(b * kVlN);
+      uint32_t taddr = 0;
+      auto filled = [&]() {            // wait for the next accumulator
+        const int b = lt & 1, u = lt >> 1;
+        const bool ok = mbar_wait(&tfull[b], u & 1);
+        if (!__all_sync(0xffffffffu, ok && !*abort_flag)) { *abort_flag = 1; return false; }
+        tc_fence_after();
+        taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(b * kVlN);
+        return true;
+      };
       auto release = [&]() {           // the accumulator has been read
+        const int b = lt & 1;
+        ++lt;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -356,12 +379,38 @@ __device__ __forceinline__ void vl_gemm(const CUtensorMap& tmA, const CUtensorMa
         }
       };
       if constexpr (!GRAD) {
+        // The sum of the runs, in order, takes the last one's place in tensor memory. (Kept in registers for the pass
+        // below, 128 of them, it made that pass unrolled code that spills: 8192 x 32000 x 256 took 710 us, not 505.)
+        if (runs == 1) {
+          if (!filled()) break;
+        } else {
+          float acc[8][16] = {};
+          bool ok = true;
+#pragma unroll 1
+          for (int r = 0; r < runs && ok; ++r) {
+            ok = filled();
+            if (!ok) break;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {          // columns past the tile's width hold nothing that is used
+              uint32_t v[16];
+              tmem_ld16(taddr + side * hn + 16 * k, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) acc[k][j] += __uint_as_float(v[j]);
+            }
+            if (r < runs - 1) release();
+          }
+          if (!ok) break;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (16 * k < hn) tmem_st16(taddr + side * hn + 16 * k, acc[k]);
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        }
         const int y = (yt >= 0 && yt < ncol) ? yt : -1;          // the target's column, if it is here
         // One pass against the target's logit, the target's own column left out; a second one, relative to the
         // half tile's largest d, only for the rare warp with a row whose weights could overflow. A NaN shows in the
         // sum. Chunks of 32 columns that are whole and hold no target of the warp's rows need no checks.
         const int c_end = min(ncol, (side + 1) * hn);
-        const float scale = 1.0f + kVlShort * 4.0f * p.nkb;        // a block of 64 is 4 steps
         float top = -INFINITY, shift = 0.0f, sum = 0.0f;
         while (true) {
           const float ref = ly + shift;
@@ -383,14 +432,14 @@ __device__ __forceinline__ void vl_gemm(const CUtensorMap& tmA, const CUtensorMa
                   const float l = __uint_as_float(v[h][j]);
                   const bool other = c + 16 * h + j < c_end && c + 16 * h + j != y;
                   if (other) high[j & 3] = fmaxf(high[j & 3], l);
-                  e[j] = other ? __expf(fmaf(l, scale, -ref)) : 0.0f;
+                  e[j] = other ? __expf(l - ref) : 0.0f;
                 }
               } else {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                   const float l = __uint_as_float(v[h][j]);
                   high[j & 3] = fmaxf(high[j & 3], l);
-                  e[j] = __expf(fmaf(l, scale, -ref));
+                  e[j] = __expf(l - ref);
                 }
               }
 #pragma unroll
@@ -421,7 +470,7 @@ __device__ __forceinline__ void vl_gemm(const CUtensorMap& tmA, const CUtensorMa
             }
             __syncwarp();                        // the next tcgen05.ld is warp-wide
           }
-          top = scale * fmaxf(fmaxf(high[0], high[1]), fmaxf(high[2], high[3]));
+          top = fmaxf(fmaxf(high[0], high[1]), fmaxf(high[2], high[3]));
           sum = (part[0] + part[1]) + (part[2] + part[3]);
           const bool far = shift == 0.0f && top - ly > kVlMaxShift;
           if (far) shift = top - ly;
@@ -430,6 +479,7 @@ __device__ __forceinline__ void vl_gemm(const CUtensorMap& tmA, const CUtensorMa
         release();                     // before the store below, which the arrival would wait for
         if (live) p.stats[static_cast<int64_t>(2 * (t.n0 / tn) + side) * p.rows_max + row] = make_float2(shift, sum);
       } else {
+        if (!filled()) break;
         __nv_bfloat16* out = p.out + static_cast<int64_t>(whole && live ? p.token[row] : 0) * p.cols + t.n0;
         float* part = whole ? nullptr : p.part + (static_cast<int64_t>(i - deal.full) * kVlM * C::CTAS + in_tile) * kVlN;
         const int c_end = min(ncol, (side + 1) * hn);

@@ -345,3 +345,55 @@ def test_token_losses_of_joined_parts(lib):
     for a, b in ((0, 7), (7, 18)):
         ref = lib.vocab_loss(X[a:b].clone(), W, y[a:b].clone(), reduction="none", dloss=w[a:b].clone())[1]
         assert torch.equal(x.grad[a:b], ref)
+
+
+@pytest.mark.parametrize("T,V,K", [(3, 40, 1032), (130, 257, 2056), (300, 511, 4104), (70, 1000, 8200), (257, 130, 16384)])
+def test_long_contractions(lib, T, V, K):
+    """More than one run of 1024 features, whole and near-equal ones, single CTAs and pairs."""
+    check(lib, *case(T, V, K, seed=15, lean=0.05))
+
+
+@pytest.mark.parametrize("T", [40, 200])
+@pytest.mark.parametrize("K", [1024, 1032, 8192, 131072])
+@pytest.mark.parametrize("kind", ["mixed", "one sign", "first 128", "last 128", "large first", "large last"])
+def test_sums_do_not_drift(lib, kind, K, T):
+    """A logit of about 12 against a target's of exactly 0, so the loss is log(1 + exp l): the error of l itself, for
+    features that grow the sum in different ways.
+
+    Bound: runs of at most 1024 features are summed in fp32. Inside a run each tensor-core step that adds something
+    truncates by at most 2^-23 of what it holds, and the additions inside a step count as 16 more: (steps + 16) 2^-23 S,
+    S = sum |x w|, steps = the most nonzero steps of one run. Adding the runs: 2^-24 S each. The loss: 2^-21 (1 + l).
+    The mean over the rows: half of 2^-23 of what each step holds is lost on average, at most a whole one: the sum over
+    the steps of the 64-bit partial sums, times 2^-23; the roundings inside steps, of the runs and of the loss are of
+    both signs, and the exponential's and the logarithm's own at most 2^-22 (1 + l)."""
+    g = torch.Generator("cuda").manual_seed(K + T)
+    x, w = torch.randn(T, K, device="cuda", generator=g), torch.randn(K, device="cuda", generator=g)
+    if kind == "mixed":
+        x, w = x + 12 / K ** 0.5 * w, w / K ** 0.5
+    elif kind == "one sign":
+        x, w = x.abs(), w.abs() * 12 * math.pi / 2 / K
+    elif kind in ("first 128", "last 128"):
+        keep = torch.arange(K, device="cuda") < 128 if kind == "first 128" else torch.arange(K, device="cuda") >= K - 128
+        x, w = torch.where(keep, x.abs(), 0.0), torch.full_like(w, 15 / 128)
+    else:
+        at = 0 if kind == "large first" else K - 1
+        w = w * 0.5 / K ** 0.5
+        x[:, at], w[at] = 6.0, 2.0
+    X, W = x.bfloat16(), torch.zeros(2, K, device="cuda", dtype=torch.bfloat16)
+    W[0] = w.bfloat16()
+    products = X.double() * W[0].double()
+    l, S = products.sum(1), products.abs().sum(1)
+    loss, _ = lib.vocab_loss(X, W, torch.ones(T, dtype=torch.int64, device="cuda"), reduction="none", need_dx=False)
+    off = loss.double() - torch.nn.functional.softplus(l)
+    steps = 8 if kind.endswith("128") else 64
+    lim = (steps + 16) * 2.0 ** -23 * S + math.ceil(K / 1024) * 2.0 ** -24 * S + 2.0 ** -21 * (1 + l.abs())
+    assert bool((off.abs() <= lim).all()), float((off.abs() / lim).max())
+    blocks = math.ceil(K / 64)
+    runs = math.ceil(blocks / 16)
+    held = torch.zeros((), dtype=torch.float64, device="cuda")
+    for r in range(runs):
+        part = products[:, 64 * (blocks * r // runs):64 * (blocks * (r + 1) // runs)]
+        part = torch.nn.functional.pad(part, (0, -part.shape[1] % 16)).unflatten(1, (-1, 16)).sum(2).cumsum(1)
+        held += part.abs().sum()
+    lim = 2.0 ** -23 * held / T + 2.0 ** -22 * (1 + l.mean())
+    assert abs(float(off.mean())) <= float(lim), (float(off.mean()), float(lim))
