@@ -935,7 +935,9 @@ int launch_rope_type(RopeParams& p, bool half, bool copy_tail, int64_t step, int
 
 // ---- vocabulary loss -------------------------------------------------------------------------------
 constexpr int kVlSms = 148;                               // CTAs of a B200 (fixed: the plan sizes the workspace)
-constexpr int64_t kVlPieceWords = int64_t(1) << 26;       // row x word weights of one piece (bf16: 128 MB)
+// A piece's rows: as many as keep its weights, its packed rows of X and its tiles' sums at 128 MB each.
+constexpr int64_t kVlPieceWords = int64_t(1) << 26;       // row x word weights, row x feature copies (bf16)
+constexpr int64_t kVlPieceTiles = int64_t(1) << 23;       // row x 128-word tiles (two 8-byte sums each)
 constexpr int64_t kVlPieceRows = 16384;
 
 // How a call is cut up, from its sizes alone, and its workspace (each part 256-byte aligned).
@@ -949,8 +951,9 @@ struct VlPlan {
 VlPlan vl_plan(int64_t T, int64_t V, int64_t K, bool grad) {
   VlPlan w{};
   w.pitch = cdiv(V, 16) * 16;
-  int64_t most = kVlPieceRows;
-  if (grad) most = std::min(most, std::max<int64_t>(kVlM, kVlPieceWords / w.pitch / kVlM * kVlM));
+  int64_t most = std::min(kVlPieceWords / K, kVlPieceTiles / cdiv(V, 128));
+  if (grad) most = std::min(most, kVlPieceWords / w.pitch);
+  most = std::min(std::max<int64_t>(kVlM, most / kVlM * kVlM), kVlPieceRows);
   w.rows = cdiv(cdiv(T, cdiv(T, most)), kVlM) * kVlM;
   w.pair = w.rows > kVlM;
   w.workers = w.pair ? kVlSms / 2 : kVlSms;

@@ -359,8 +359,10 @@ int qlora_rope(const qlora_rope_tensor* x, int nx, int dtype, int64_t B, int64_t
  * as ignored. fp32 logits and sums (a logit is the sum of tensor-core sums over at most 1024 features each, off by up
  * to 2e-6 of sum |x w|); the softmax weights are rounded to bf16 for the gradient's product.
  * Rules: T, V >= 1 (V < 2^30), K % 8 == 0, 8 <= K <= 2^20. `workspace` >= qlora_vocab_loss_workspace(T, V, K,
- * dX != NULL): with dX at most 128 MB for the weights of one piece of the tokens (two bytes per token and word of
- * it; more where 128 tokens, the smallest piece, need more), and 58 MB of partial sums, a copy of the piece's rows of X, and 12 bytes per token. Deterministic.
+ * dX != NULL): 12 bytes per token, and for one piece of the tokens at most 128 MB for a copy of its rows of X (kept for
+ * calls that leave tokens out; the size cannot tell) and 128 MB for its tiles' sums; with dX also at most 128 MB for its
+ * weights (two bytes per token and word of it) and 59 MB of partial sums. Each of the 128 MB is more where 128 tokens,
+ * the smallest piece, need more. Deterministic.
  */
 enum { QLORA_LOSS_NONE = 0, QLORA_LOSS_SUM = 1, QLORA_LOSS_MEAN = 2 };
 int qlora_vocab_loss_workspace(int64_t T, int64_t V, int64_t K, int gradient, size_t* bytes);

@@ -397,3 +397,12 @@ def test_sums_do_not_drift(lib, kind, K, T):
         held += part.abs().sum()
     lim = 2.0 ** -23 * held / T + 2.0 ** -22 * (1 + l.mean())
     assert abs(float(off.mean())) <= float(lim), (float(off.mean()), float(lim))
+
+
+def test_pieces_of_long_rows(lib):
+    """512 rows of 2^17 features are what a piece's copy of X takes: three pieces, with the gradient and without, tokens
+    left out and none."""
+    X, W, y = case(1100, 40, 1 << 17, seed=16, lean=0.0, scale=0.03)
+    check(lib, X, W, y)
+    y[::5] = -100
+    check(lib, X, W, y)

@@ -111,3 +111,16 @@ def test_codebook_linear_refusals(q):
 
 def test_new_status_has_its_message(q):
     assert b"vocabulary" in q.lib.qlora_error_string(-11)
+
+
+@pytest.mark.parametrize("gradient", [False, True])
+@pytest.mark.parametrize("T", [1, 128, 8192, 16384, 65536, 1 << 20])
+@pytest.mark.parametrize("V,K", [(32000, 4096), (131072, 8192), (1000000, 8192), (500, 1 << 20), (1 << 21, 64)])
+def test_vocab_loss_workspace_is_bounded(q, gradient, T, V, K):
+    """As documented: 12 bytes a token; a piece's rows of X, its tiles' sums (16 bytes per row and tile of 128 words at
+    least) and its weights, each 128 MB or what 128 rows need; 59 MB of partial sums; 256 bytes of rounding a part."""
+    most = lambda per_row: max(1 << 27, 128 * per_row)  # noqa: E731
+    limit = 12 * T + most(2 * K) + most(16 * -(-V // 128)) + 12 * 16384 + (1 << 13)
+    if gradient:
+        limit += most(2 * (V + 15)) + 3 * 148 * 128 * 256 * 4
+    assert q.vocab_loss_workspace_bytes(T, V, K, gradient) <= limit
