@@ -1453,7 +1453,7 @@ int qlora_codebook_linear(const void* X, int64_t T, const void* codes, const flo
   for (float& level : cb.levels) level *= factor;
   p.unscale = 1.0f / factor;
   p.Y = static_cast<__nv_bfloat16*>(Y);
-  // one or two tokens whose X fits in shared memory (K up to 24,500, or 12,200 for two)
+  // one or two tokens whose X fits in shared memory (48 KB beside the sums: K up to 24576, or 12288 for two)
   if (T <= kC1Tokens && c1_x_bytes(T, K / 64) <= kC1XBytes) return launch_codebook_linear1(p, cb, sms, st);
   if (T <= 8) return launch_codebook_linear4<1>(p, cb, sms, st);
   return launch_codebook_linear4<2>(p, cb, sms, st);

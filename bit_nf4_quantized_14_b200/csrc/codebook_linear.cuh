@@ -23,8 +23,9 @@
 namespace qnf4 {
 
 constexpr int kClMaxTokens = 64;
-// Measured (a weight in HBM, calls back to back): 22016 x 8192 at one token 24 us (4.2 TB/s), 4 tokens 28, 16
-// tokens 40; 8192 x 8192 at one token 12.5 us. The plain copy's rate would be 15.5 and 5.8 us.
+// Measured (six weights in turn, replayed back to back): 22016 x 8192 at one token 23 us (4.4 TB/s), 4 tokens 27, 16
+// tokens 39, 17 to 32 tokens 69 to 74, 64 tokens 145 (every group of 16 looks the weight up again); 8192 x 8192 12, 13,
+// 17, 31, 59 us. The plain copy's rate would be 15.5 and 5.8 us.
 //
 // Shared memory: the table (256 entries of 256 bytes, the lane copies in the first 128) sits at shared address
 // 64 KB, so one byte permute forms a lookup's address; the stream's slots lie above it, sums (and X) below.
