@@ -237,7 +237,6 @@ __device__ __forceinline__ void vl_gemm(const CUtensorMap& tmA, const CUtensorMa
   asm volatile("fence.proxy.async;" ::: "memory");     // what earlier kernels stored, for this one's TMA
   const uint32_t tmem_base = *tmem_slot;
   const uint32_t idesc = idesc_bf16(kVlM * C::CTAS, 16, false, GRAD) - (2u << 17) + (static_cast<uint32_t>(p.bn >> 3) << 17);
-  int issued = 0;
 
   const int rows = vl_rows(p.count, p.r0, p.rows_max);
   const int tiles_m = (rows + kVlM * C::CTAS - 1) / (kVlM * C::CTAS);
@@ -290,9 +289,12 @@ __device__ __forceinline__ void vl_gemm(const CUtensorMap& tmA, const CUtensorMa
             for (int a = 0; a < C::BROWS / 64; ++a)
               vl_tma<PAIR>(sB + s * C::B_BYTES + a * 8192, &tmB, bar, t.n0 + rank * bn_cta + 64 * a, kb * kVlK);
           }
-          issued = it + 1;
         }
       }
+      // This CTA's copies have landed once they are used. After a wait that gave up nobody uses them: then a limit far
+      // above a copy's time stands for that. (A pair's copies count on the first CTA's barriers, but the second may have
+      // run ahead of it, so neither CTA's copies can be told by those.)
+      for (int last = max(it - ST, 0); last < it && mbar_wait_short(&empty[last % ST], (last / ST) & 1); ++last) {}
     }
   } else if (warp == 1) {
     // ------------------------------- MMA issuer (the first CTA) -------------------------------
@@ -509,13 +511,13 @@ __device__ __forceinline__ void vl_gemm(const CUtensorMap& tmA, const CUtensorMa
   }
 
   // ------------------------------- teardown -------------------------------
-  // every MMA of the pair, and the arrivals that its commits make in either CTA, are done
+  // every MMA of the pair, and the arrivals that its commits make in either CTA, are done (again with a limit where
+  // that wait gave up)
   if (warp == 1 && lane == 0 && !mbar_wait(drain, 0)) *abort_flag = 1;
   tc_fence_before();
   __syncthreads();
   if (*abort_flag) {
-    if (warp == 0 && lane == 0 && rank == 0)
-      for (int it = (issued > ST ? issued - ST : 0); it < issued; ++it) mbar_wait_short(&full[it % ST], (it / ST) & 1);
+    if (warp == 1 && lane == 0) mbar_wait_short(drain, 0);
     __syncthreads();
   }
   if constexpr (PAIR) vl_cluster_sync();    // neither CTA leaves while the other's copies, MMAs or arrivals reach it

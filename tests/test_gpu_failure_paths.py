@@ -71,3 +71,23 @@ def test_injected_launch_failure(lib, monkeypatch):
     monkeypatch.delenv("QLORA_FAULT_INJECT")
     assert lib.get_status() == 0
     assert torch.equal(Y1, Y3) and torch.equal(U1, U3)
+
+
+@pytest.mark.parametrize("T", [60, 200])
+def test_vocabulary_loss_unwinds_after_a_wait_that_gives_up(lib, T):
+    """A limit of 1 us is shorter than the gradient's tile takes along 60,000 words: its epilogue gives up while copies
+    and MMAs are in flight, the kernel unwinds (single CTAs and pairs), and the next call is right again."""
+    g = torch.Generator("cuda").manual_seed(T)
+    W = (torch.randn(60000, 4096, device="cuda", generator=g) * 0.1).bfloat16()
+    X = torch.randn(T, 4096, device="cuda", generator=g).bfloat16()
+    y = torch.randint(0, 60000, (T,), device="cuda", generator=g)
+    ref = lib.vocab_loss(X, W, y)
+    assert lib.get_status() == 0
+    try:
+        lib.set_wait_limit(1000)
+        lib.vocab_loss(X, W, y)
+        assert lib.get_status() == lib.STATUS_TIMEOUT
+    finally:
+        lib.set_wait_limit(0)
+    again = lib.vocab_loss(X, W, y)
+    assert lib.get_status() == 0 and torch.equal(again[0], ref[0]) and torch.equal(again[1], ref[1])
