@@ -391,7 +391,8 @@ def _nf4_levels() -> tuple:
 def codebook_linear(X: torch.Tensor, codes: torch.Tensor, absmax: torch.Tensor, N: int, levels,
                     out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Y = X W^T (T x N bf16) for X (T x K bf16, T <= CODEBOOK_LINEAR_MAX_TOKENS) and the N x K weight that
-    codebook_quantize(w, levels) wrote as codes and absmax (qlora_codebook_linear). K % 64 == 0."""
+    codebook_quantize(w, levels) wrote as codes and absmax (qlora_codebook_linear). K % 64 == 0; all of them begin on
+    16 bytes."""
     if stream is not None:
         with _given(stream, X):
             return codebook_linear(X, codes, absmax, N, levels, out)

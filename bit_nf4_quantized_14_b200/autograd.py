@@ -106,7 +106,7 @@ class VocabLossFn(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, head, targets, ignore_index: int, reduction: str):
-        x2 = x.reshape(-1, x.shape[-1]).to(torch.bfloat16).contiguous()
+        x2 = _aligned(x.reshape(-1, x.shape[-1]).to(torch.bfloat16).contiguous())
         need = ctx.needs_input_grad[0] and reduction != "none"
         loss, dx = _vocab_loss(x2, head, targets.reshape(-1).contiguous(), ignore_index, reduction, need_dx=need)
         ctx.ignore_index, ctx.reduction, ctx.like = ignore_index, reduction, x.shape
@@ -134,7 +134,7 @@ def vocab_loss(x: torch.Tensor, head: torch.Tensor, targets: torch.Tensor, ignor
                reduction: str = "mean") -> torch.Tensor:
     """Differentiable vocabulary loss of hidden states x (..., K) with a frozen bf16 head (V x K) and targets
     (...): the cross entropy of x head^T without its logits (see bit_nf4_quantized_14_b200.vocab_loss). x is taken
-    in bf16. A head that wants a gradient is refused: it would get none."""
+    in bf16, copied where it does not begin on 16 bytes. A head that wants a gradient is refused: it would get none."""
     if head.requires_grad and torch.is_grad_enabled():
         raise ValueError("vocab_loss: the head is frozen and gets no gradient (detach it)")
     return VocabLossFn.apply(x, head, targets, ignore_index, reduction)

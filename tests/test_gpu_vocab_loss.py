@@ -406,3 +406,16 @@ def test_pieces_of_long_rows(lib):
     check(lib, X, W, y)
     y[::5] = -100
     check(lib, X, W, y)
+
+
+def test_hidden_state_that_begins_anywhere(lib):
+    """One token's features behind 9 others of its row: a contiguous view 18 bytes in."""
+    from bit_nf4_quantized_14_b200.autograd import vocab_loss
+    X, W, y = case(1, 300, 64, seed=17)
+    row = torch.cat([torch.zeros(1, 9, dtype=torch.bfloat16, device="cuda"), X], -1).requires_grad_()
+    for red in ("mean", "none"):
+        row.grad = None
+        loss = vocab_loss(row[:, 9:], W, y, reduction=red)
+        loss.sum().backward()
+        ref, dref = lib.vocab_loss(X, W, y, reduction=red)
+        assert torch.equal(loss.detach(), ref) and torch.equal(row.grad[:, 9:], dref) and not row.grad[:, :9].any()
