@@ -1043,6 +1043,8 @@ int run_vocab_loss(const __nv_bfloat16* X, int64_t T, const __nv_bfloat16* W, in
     p.bn = L.bn;
     p.tiles_n = tiles_v;
     p.nkb = static_cast<int>(cdiv(K, kVlK));
+    p.runs = p.nkb <= kVlRun / 2 ? 1 : std::max(2, static_cast<int>(cdiv(p.nkb, kVlRun)));
+    p.run_scale = 1.0f + kVlShort * (kVlK / 16) * p.nkb / p.runs;
     p.target = target + r0;
     p.w = W;
     p.w_pitch = static_cast<int>(K);

@@ -58,9 +58,14 @@ constexpr int kVlThreads = 10 * 32;       // TMA, MMA, 8 epilogue warps
 // The tensor cores drop what does not fit an accumulator's 24 bits, towards zero: in one run over K a logit loses a share of
 // itself that grows with K and depends on the data (K = 8192, relative: features of random signs 8e-6, of one sign
 // 3.4e-5, one large feature first 1.5e-5, last 0; of one sign at K = 2^20 6.7e-3). So a logit is the fp32 sum of near-equal
-// runs of at most 16 blocks (64 steps): 1e-6, of one sign 2e-6, at any K. It costs 1 to 4 % of a call (8 blocks: half the
-// error, 4 to 8 %).
+// runs of at most 16 blocks. Such a run of 64 steps loses between nothing (large features last, or zeros) and 2.1e-6 of
+// itself (one sign), with random signs 1.06e-6: that middle is put back, 1.65e-8 a step, which leaves any data within
+// 1.1e-6 at any K, and random signs within 2e-7. (Without it tokens of small losses, whose error is the logits' own, were
+// up to 2.6e-6 off, one or two tokens of K = 6360.) Up to 8 blocks are one run as it is: 5e-7 at most where signs are
+// random, and the epilogue binds there (with a factor on every logit 700 x 32000 x 64 took 39 us, not 35). The runs cost
+// 1 to 4 % of a call; of 8 blocks 4 to 8 %.
 constexpr int kVlRun = 16;
+constexpr float kVlShort = 1.65e-8f;
 constexpr float kVlMaxShift = 40.0f;      // exp(40) x any vocabulary stays far inside fp32 and bf16
 constexpr unsigned kStatusTarget = 4u;
 
@@ -70,6 +75,8 @@ struct VlParams {
   int copied;                   // <0>: rows live in the packed copy (second map) when count < copied
   int cols, bn;                 // columns (words, or features of dX) and columns per tile
   int tiles_n, nkb;             // column tiles; contraction blocks of 64
+  int runs;                     // <0>: runs of blocks that are summed in fp32 (<1>: one)
+  float run_scale;              // <0>: factor on every run, where there are several
   const __nv_bfloat16* w;       // <0>: W, for prefetches, and its row pitch
   int w_pitch;
   const int* target;            // <0>: per row
@@ -245,7 +252,7 @@ __device__ __forceinline__ void vl_gemm(const CUtensorMap& tmA, const CUtensorMa
   const int num_items = deal.full + deal.rest * deal.cuts;
   const int bn_cta = p.bn / C::CTAS;
   // accumulator fills per item: the runs of a logit, near-equal ones; run r begins at block run_at(r)
-  const int runs = GRAD ? 1 : (p.nkb + kVlRun - 1) / kVlRun;
+  const int runs = GRAD ? 1 : p.runs;
   auto run_at = [&](int r) { return static_cast<int>(static_cast<int64_t>(p.nkb) * r / runs); };
   struct Item { int m0, n0, kb0, kb1; };
   auto item = [&](int i) {
@@ -398,7 +405,7 @@ __device__ __forceinline__ void vl_gemm(const CUtensorMap& tmA, const CUtensorMa
               tmem_ld16(taddr + side * hn + 16 * k, v);
               tmem_wait_ld();
 #pragma unroll
-              for (int j = 0; j < 16; ++j) acc[k][j] += __uint_as_float(v[j]);
+              for (int j = 0; j < 16; ++j) acc[k][j] = fmaf(__uint_as_float(v[j]), p.run_scale, acc[k][j]);
             }
             if (r < runs - 1) release();
           }

@@ -357,7 +357,7 @@ int qlora_rope(const qlora_rope_tensor* x, int nx, int dtype, int64_t B, int64_t
  *   dX     T x K bf16 (written; zero rows for ignored tokens), or NULL: loss only
  * A target that is neither ignore_index nor in [0, V) sets QLORA_STATUS_TARGET; its token is then treated
  * as ignored. fp32 logits and sums (a logit is the sum of tensor-core sums over at most 1024 features each, off by up
- * to 2e-6 of sum |x w|); the softmax weights are rounded to bf16 for the gradient's product.
+ * to 1.1e-6 of sum |x w|); the softmax weights are rounded to bf16 for the gradient's product.
  * Rules: T, V >= 1 (V < 2^30), K % 8 == 0, 8 <= K <= 2^20. `workspace` >= qlora_vocab_loss_workspace(T, V, K,
  * dX != NULL): 12 bytes per token, and for one piece of the tokens at most 128 MB for a copy of its rows of X (kept for
  * calls that leave tokens out; the size cannot tell) and 128 MB for its tiles' sums; with dX also at most 128 MB for its

@@ -363,6 +363,7 @@ def test_sums_do_not_drift(lib, kind, K, T):
     Bound: runs of at most 1024 features are summed in fp32. Inside a run each tensor-core step that adds something
     truncates by at most 2^-23 of what it holds, and the additions inside a step count as 16 more: (steps + 16) 2^-23 S,
     S = sum |x w|, steps = the most nonzero steps of one run. Adding the runs: 2^-24 S each. The loss: 2^-21 (1 + l).
+    The kernel puts back 1.65e-8 of a run per step, which may not be missing: 1.06e-6 of each run of 64 steps more.
     The mean over the rows: half of 2^-23 of what each step holds is lost on average, at most a whole one: the sum over
     the steps of the 64-bit partial sums, times 2^-23; the roundings inside steps, of the runs and of the loss are of
     both signs, and the exponential's and the logarithm's own at most 2^-22 (1 + l)."""
@@ -386,16 +387,17 @@ def test_sums_do_not_drift(lib, kind, K, T):
     loss, _ = lib.vocab_loss(X, W, torch.ones(T, dtype=torch.int64, device="cuda"), reduction="none", need_dx=False)
     off = loss.double() - torch.nn.functional.softplus(l)
     steps = 8 if kind.endswith("128") else 64
-    lim = (steps + 16) * 2.0 ** -23 * S + math.ceil(K / 1024) * 2.0 ** -24 * S + 2.0 ** -21 * (1 + l.abs())
-    assert bool((off.abs() <= lim).all()), float((off.abs() / lim).max())
     blocks = math.ceil(K / 64)
     runs = math.ceil(blocks / 16)
+    parts = [products[:, 64 * (blocks * r // runs):64 * (blocks * (r + 1) // runs)] for r in range(runs)]
+    back = 64 * 1.65e-8 * sum(p.sum(1).abs() for p in parts)
+    lim = (steps + 16) * 2.0 ** -23 * S + back + math.ceil(K / 1024) * 2.0 ** -24 * S + 2.0 ** -21 * (1 + l.abs())
+    assert bool((off.abs() <= lim).all()), float((off.abs() / lim).max())
     held = torch.zeros((), dtype=torch.float64, device="cuda")
-    for r in range(runs):
-        part = products[:, 64 * (blocks * r // runs):64 * (blocks * (r + 1) // runs)]
+    for part in parts:
         part = torch.nn.functional.pad(part, (0, -part.shape[1] % 16)).unflatten(1, (-1, 16)).sum(2).cumsum(1)
         held += part.abs().sum()
-    lim = 2.0 ** -23 * held / T + 2.0 ** -22 * (1 + l.mean())
+    lim = 2.0 ** -23 * held / T + back.mean() + 2.0 ** -22 * (1 + l.mean())
     assert abs(float(off.mean())) <= float(lim), (float(off.mean()), float(lim))
 
 
